@@ -372,6 +372,167 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_noalloc(const uint16_t *q,
                                              uint16_t *out, float *lse, void *stream);
 
 /* ------------------------------------------------------------------------
+ * The 8-bit KV cache.
+ *
+ * The paged cache with K and V in e4m3 and one power-of-two scale per block of
+ * tokens and KV group, half the bytes of the bf16 cache.  The pages have no
+ * counterpart; the layout follows the decode section above:
+ *
+ *   k_cache8,
+ *   v_cache8      [num_pages, 64, Hkv, D] e4m3 bytes
+ *   kv_exp        [num_pages, 64 / scale_block, Hkv, 2] uint8: the scale
+ *                 exponents of K ([..., 0]) and V ([..., 1]); a cached value
+ *                 is e4m3(byte) * 2^(exponent - 127).
+ *   scale_block   tokens that share a scale: 16, 32 or 64
+ *   num_pages     < 2^25 (a cache row is addressed by 31 bits)
+ *
+ * dsa_kv8_append writes new tokens into it.  Sequence b has seq_lens[b]
+ * tokens, its new ones included; they are the last of them, and their pages
+ * are in its block-table row already (dsa_pages_extend).  For each block and
+ * group that new tokens x fall into, the exponent becomes the least e with
+ * max|x| <= 448 * 2^(e - 127), not below the exponent there when older tokens
+ * of the sequence are in the block, and within 87..167 (2^-40 .. 2^40; larger
+ * values saturate at 448 * 2^40).  The new bytes are the nearest e4m3 values
+ * (ties to even); where the exponent grew, the older bytes are divided by the
+ * power of two and rounded again, which changes only values below the least
+ * normal e4m3.  The result depends on the order in which tokens are appended
+ * only through those values.
+ *
+ *   K, V          [n_tokens, Hkv, D] bf16, rows ld_k and ld_v elements apart
+ *                 (>= Hkv * D, a multiple of 8; pointers 16-byte aligned)
+ *   cu_seqlens    device int32 [nseq + 1]: sequence b's new tokens are rows
+ *                 cu_seqlens[b] .. cu_seqlens[b+1]-1 (ascending; empty
+ *                 sequences allowed; rows from cu_seqlens[nseq] on are not
+ *                 used), or NULL: one new token per sequence, n_tokens == nseq
+ *   block_table   [nseq, max_pages], seq_lens [nseq]
+ *   k8, k_scale,
+ *   k8_cache,
+ *   k_scale_cache the new tokens' indexer keys [n_tokens, dI] and scales
+ *                 [n_tokens], copied to their places in [num_pages, 64, dI]
+ *                 and [num_pages, 64]; all four or none (then dI is unused)
+ * A token at a negative position, past the block table, or on a page outside
+ * [0, num_pages) is dropped.  A page that receives tokens must belong to one
+ * sequence only (dsa_pages_fork keeps it so).  Slots behind a sequence's last
+ * token are left as they were.  Supported: D in {64, 128}, Hkv <= 1024, dI in
+ * {32, 64, 128}.
+ * ------------------------------------------------------------------------ */
+DSA_API dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint16_t *V, int64_t ld_v,
+                            const uint8_t *k8, const float *k_scale, const int32_t *cu_seqlens, int nseq,
+                            int n_tokens, const int32_t *seq_lens, const int32_t *block_table, int max_pages,
+                            int num_pages, int Hkv, int D, int dI, int scale_block, uint8_t *k_cache8,
+                            uint8_t *v_cache8, uint8_t *kv_exp, uint8_t *k8_cache, float *k_scale_cache,
+                            void *stream);
+
+/* Decode stage 3 over the 8-bit cache: as dsa_sparse_gqa_decode_attention,
+ * with the same treatment of index entries, pages and empty rows, and without
+ * a workspace (a row's splits are joined on chip).  kv_exp is 2-byte aligned;
+ * q, out and the caches are 16-byte aligned. */
+DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_kv8(const uint16_t *q, const uint8_t *k_cache8,
+                                                 const uint8_t *v_cache8, const uint8_t *kv_exp, int scale_block,
+                                                 const int32_t *block_table, int max_pages, int num_pages,
+                                                 const int32_t *seq_lens, const int32_t *idx, int B, int Hq,
+                                                 int Hkv, int D, int k, float sm_scale, uint16_t *out, float *lse,
+                                                 void *stream);
+
+/* Several query tokens per sequence over the 8-bit cache (a chunk of a prompt,
+ * drafted tokens): packed query rows as in dsa_sparse_gqa_prefill_varlen.
+ * Sequence b's query rows are cu_seqlens[b] .. cu_seqlens[b+1]-1 and are the
+ * last of its seq_lens[b] cached tokens: row r of it stands at position t =
+ * seq_lens[b] - cu_seqlens[b+1] + r and sees the cached tokens 0..t.  idx rows
+ * hold positions within the sequence; only the first min(k, t+1) entries are
+ * visited and entries outside [0, t] are skipped.
+ *   Q, O [n_rows, Hq, D], idx [n_rows, k], lse [n_rows, Hq] (may be NULL):
+ *        packed rows row_begin .. row_begin + n_rows - 1
+ *   block_table [nseq, max_pages], seq_lens [nseq]
+ * Rows outside [cu_seqlens[0], cu_seqlens[nseq]) are left as they were. */
+DSA_API dsa_status_t dsa_sparse_gqa_prefill_kv8(const uint16_t *Q, const uint8_t *k_cache8, const uint8_t *v_cache8,
+                                        const uint8_t *kv_exp, int scale_block, const int32_t *block_table,
+                                        int max_pages, int num_pages, const int32_t *seq_lens, const int32_t *idx,
+                                        const int32_t *cu_seqlens, int nseq, int row_begin, int n_rows, int Hq,
+                                        int Hkv, int D, int k, float sm_scale, uint16_t *O, float *lse,
+                                        void *stream);
+
+/* dsa_sparse_gqa_decode with K and V in the 8-bit cache: scores -> top-k ->
+ * attention of one new token per sequence. */
+DSA_API size_t dsa_decode_kv8_workspace_size(int B, int max_seq_len, int k);
+DSA_API dsa_status_t dsa_sparse_gqa_decode_kv8(const uint16_t *q, const uint8_t *q8, const float *q_scale,
+                                       const float *w, const uint8_t *k8_cache, const float *k_scale_cache,
+                                       const uint8_t *k_cache8, const uint8_t *v_cache8, const uint8_t *kv_exp,
+                                       int scale_block, const int32_t *block_table, int max_pages, int num_pages,
+                                       const int32_t *seq_lens, int max_seq_len, int B, int Hq, int Hkv, int D,
+                                       int HI, int dI, int k, float sm_scale, void *ws, size_t ws_bytes,
+                                       uint16_t *out, int32_t *idx_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of a cache.
+ *
+ * A pool of num_pages pages and n_slots sequence slots:
+ *   refcount      [num_pages] int32: how many sequences hold the page, 0 =
+ *                 free (a negative count is never granted)
+ *   block_table   [n_slots, max_pages] int32, -1 past a sequence's pages
+ *   seq_lens      [n_slots] int32, 0 = empty slot
+ * All three start as zeros (block_table: -1) and are changed by the calls
+ * below, on the device; a call sees the state that earlier calls on its stream
+ * left.  Free pages are granted lowest id first, to the entries of a call in
+ * their order, so every result is determined.  A page that is only partly
+ * filled belongs to one sequence: forking copies it, so that appending never
+ * writes to a page that another sequence reads.
+ *
+ * Cache buffers are given as host arrays of n_bufs <= 8 device pointers and
+ * page sizes in bytes (1 .. 2^24): page p of buffer i is page_bytes[i] bytes
+ * at bases[i] + p * page_bytes[i].  Any cache of this library can be given,
+ * bf16 or 8-bit; pages of a multiple of 16 bytes on 16-byte boundaries move
+ * 16 bytes at a time.
+ *
+ * status [n] int32 receives, per entry: 0 done; 1 not enough free pages (an
+ * entry that needs pages is refused when the pages wanted up to and including
+ * it are more than there are free); 2 refused (a slot out of range, a length
+ * the call does not allow, a slot named by an earlier entry).  A refused
+ * entry's sequence is unchanged.  n <= 1024 per call
+ * (DSA_ERR_UNSUPPORTED_SHAPE above), num_pages < 2^25.
+ *
+ *   dsa_pages_extend  slots[i] grows to new_lens[i] tokens (>= its length, <=
+ *                     64 * max_pages) and gets the pages that takes.
+ *   dsa_pages_fork    children[i], an empty slot, becomes a copy of
+ *                     parents[i]: full pages are shared (their counts rise), a
+ *                     partly filled last page is copied to a page of its own
+ *                     in every buffer.  Lengths are read as they are before
+ *                     the call.
+ *   dsa_pages_free    slots[i] becomes empty; pages that no other sequence
+ *                     holds become free.  Slots out of range are skipped, one
+ *                     named twice is freed once.
+ *   dsa_pages_copy    page src[i] to page dst[i] in every buffer.  Pairs with
+ *                     an id outside [0, num_pages) or with src[i] == dst[i]
+ *                     are skipped; a page may be the source of several pairs,
+ *                     and the destination of one that is no pair's source
+ *                     (its bytes are unspecified otherwise).  n any.
+ *   dsa_pages_compact brings the n_used pages in use to the ids 0..n_used-1:
+ *                     the k-th used page from n_used on moves to the k-th free
+ *                     id below it, all others stay.  page_map [num_pages]
+ *                     receives each page's new id (-1: it was free), for
+ *                     references kept elsewhere; n_used one int32.  The table
+ *                     and the counts may be written in place (equal pointers)
+ *                     or to other buffers.  ws: dsa_pages_compact_workspace_
+ *                     size(num_pages) bytes, 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+DSA_API dsa_status_t dsa_pages_extend(const int32_t *slots, const int32_t *new_lens, int n, int32_t *block_table,
+                              int n_slots, int max_pages, int32_t *seq_lens, int32_t *refcount, int num_pages,
+                              int32_t *status, void *stream);
+DSA_API dsa_status_t dsa_pages_fork(void *const *bases, const size_t *page_bytes, int n_bufs, const int32_t *parents,
+                            const int32_t *children, int n, int32_t *block_table, int n_slots, int max_pages,
+                            int32_t *seq_lens, int32_t *refcount, int num_pages, int32_t *status, void *stream);
+DSA_API dsa_status_t dsa_pages_free(const int32_t *slots, int n, int32_t *block_table, int n_slots, int max_pages,
+                            int32_t *seq_lens, int32_t *refcount, int num_pages, void *stream);
+DSA_API dsa_status_t dsa_pages_copy(void *const *bases, const size_t *page_bytes, int n_bufs, const int32_t *src,
+                            const int32_t *dst, int n, int num_pages, void *stream);
+DSA_API size_t dsa_pages_compact_workspace_size(int num_pages);
+DSA_API dsa_status_t dsa_pages_compact(void *const *bases, const size_t *page_bytes, int n_bufs,
+                               const int32_t *block_table, int32_t *block_table_out, int n_slots, int max_pages,
+                               const int32_t *seq_lens, const int32_t *refcount, int32_t *refcount_out,
+                               int num_pages, int32_t *page_map, int32_t *n_used, void *ws, size_t ws_bytes,
+                               void *stream);
+
+/* ------------------------------------------------------------------------
  * Read-bandwidth probe (diagnostic, not part of the layer; the pages have no
  * counterpart).  Reads `bytes` bytes of `buf` `reps` times with 16-byte loads
  * cached in L2 only (the load form the attention's gathers use), spread over

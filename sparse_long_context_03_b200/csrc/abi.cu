@@ -368,6 +368,227 @@ dsa_status_t dsa_sparse_gqa_decode(const uint16_t *q, const uint8_t *q8, const f
     return cuda_status(e);
 }
 
+// ---------------------------------------------------------------------------
+// the 8-bit KV cache
+// ---------------------------------------------------------------------------
+
+static bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Cache rows are addressed by 31 bits: page * 64 + slot.
+static bool kv8_cache_supported(int num_pages, int scale_block) {
+    return num_pages < (1 << 25) && (scale_block == 16 || scale_block == 32 || scale_block == 64);
+}
+
+dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint16_t *V, int64_t ld_v, const uint8_t *k8,
+                            const float *k_scale, const int32_t *cu_seqlens, int nseq, int n_tokens,
+                            const int32_t *seq_lens, const int32_t *block_table, int max_pages, int num_pages,
+                            int Hkv, int D, int dI, int scale_block, uint8_t *k_cache8, uint8_t *v_cache8,
+                            uint8_t *kv_exp, uint8_t *k8_cache, float *k_scale_cache, void *stream) {
+    const Range range(__func__);
+    if (nseq < 0 || n_tokens < 0 || max_pages < 1 || num_pages < 1 || Hkv < 1) return DSA_ERR_INVALID_ARG;
+    if (cu_seqlens == nullptr && n_tokens != nseq) return DSA_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || Hkv > 1024 || !kv8_cache_supported(num_pages, scale_block) || nseq > (1 << 29))
+        return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (nseq == 0 || n_tokens == 0) return DSA_OK;
+    const int given = (k8 != nullptr) + (k_scale != nullptr) + (k8_cache != nullptr) + (k_scale_cache != nullptr);
+    if (given != 0 && given != 4) return DSA_ERR_INVALID_ARG;
+    if (given == 4 && dI != 32 && dI != 64 && dI != 128) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!K || !V || !seq_lens || !block_table || !k_cache8 || !v_cache8 || !kv_exp) return DSA_ERR_INVALID_ARG;
+    if (ld_k < (int64_t)Hkv * D || ld_v < (int64_t)Hkv * D || ld_k % 8 != 0 || ld_v % 8 != 0)
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(k_cache8, 16) || !aligned(v_cache8, 16) || !aligned(k8, 16) ||
+        !aligned(k8_cache, 16) || !aligned(k_scale, 4) || !aligned(k_scale_cache, 4))
+        return DSA_ERR_INVALID_ARG;
+    return cuda_status(dsa::launch_kv8_append(K, ld_k, V, ld_v, k8, k_scale, cu_seqlens, nseq, n_tokens, seq_lens,
+                                              block_table, max_pages, num_pages, Hkv, D, dI, scale_block, k_cache8,
+                                              v_cache8, kv_exp, k8_cache, k_scale_cache, as_stream(stream)));
+}
+
+static dsa_status_t check_kv8_attention(const void *q, const void *k_cache8, const void *v_cache8, const void *kv_exp,
+                                        int scale_block, const void *block_table, int max_pages, int num_pages,
+                                        const void *seq_lens, const void *idx, int rows, int Hq, int Hkv, int D,
+                                        int k, const void *out) {
+    if (rows < 0 || k < 1 || Hq < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1) return DSA_ERR_INVALID_ARG;
+    if (!dsa::attention_shape_supported(Hq, Hkv, D) || !kv8_cache_supported(num_pages, scale_block) ||
+        max_pages >= (1 << 25))
+        return DSA_ERR_UNSUPPORTED_SHAPE;
+    if ((int64_t)rows * Hkv >= (1ll << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;  // one CTA per (row, group)
+    if (rows == 0) return DSA_OK;
+    if (!q || !k_cache8 || !v_cache8 || !kv_exp || !block_table || !seq_lens || !idx || !out)
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache8, 16) || !aligned(v_cache8, 16) ||
+        !aligned(kv_exp, 2))
+        return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+dsa_status_t dsa_sparse_gqa_decode_attention_kv8(const uint16_t *q, const uint8_t *k_cache8, const uint8_t *v_cache8,
+                                                 const uint8_t *kv_exp, int scale_block, const int32_t *block_table,
+                                                 int max_pages, int num_pages, const int32_t *seq_lens,
+                                                 const int32_t *idx, int B, int Hq, int Hkv, int D, int k,
+                                                 float sm_scale, uint16_t *out, float *lse, void *stream) {
+    const Range range(__func__);
+    const dsa_status_t st = check_kv8_attention(q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages,
+                                                num_pages, seq_lens, idx, B, Hq, Hkv, D, k, out);
+    if (st != DSA_OK) return st;
+    return cuda_status(dsa::launch_sparse_kv8(q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages,
+                                              num_pages, seq_lens, idx, nullptr, 0, 0, B, Hq, Hkv, D, k, sm_scale,
+                                              out, lse, as_stream(stream)));
+}
+
+dsa_status_t dsa_sparse_gqa_prefill_kv8(const uint16_t *Q, const uint8_t *k_cache8, const uint8_t *v_cache8,
+                                        const uint8_t *kv_exp, int scale_block, const int32_t *block_table,
+                                        int max_pages, int num_pages, const int32_t *seq_lens, const int32_t *idx,
+                                        const int32_t *cu_seqlens, int nseq, int row_begin, int n_rows, int Hq,
+                                        int Hkv, int D, int k, float sm_scale, uint16_t *O, float *lse,
+                                        void *stream) {
+    const Range range(__func__);
+    if (cu_seqlens == nullptr || nseq < 1 || row_begin < 0 || (int64_t)row_begin + n_rows >= (1ll << 31))
+        return DSA_ERR_INVALID_ARG;
+    const dsa_status_t st = check_kv8_attention(Q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages,
+                                                num_pages, seq_lens, idx, n_rows, Hq, Hkv, D, k, O);
+    if (st != DSA_OK) return st;
+    return cuda_status(dsa::launch_sparse_kv8(Q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages,
+                                              num_pages, seq_lens, idx, cu_seqlens, nseq, row_begin, n_rows, Hq, Hkv,
+                                              D, k, sm_scale, O, lse, as_stream(stream)));
+}
+
+size_t dsa_decode_kv8_workspace_size(int B, int max_seq_len, int k) {
+    if (B < 0 || max_seq_len < 0 || k < 1) return 0;
+    return decode_ws_layout(B, max_seq_len, 1, 1, 0, k).attn_off;
+}
+
+dsa_status_t dsa_sparse_gqa_decode_kv8(const uint16_t *q, const uint8_t *q8, const float *q_scale, const float *w,
+                                       const uint8_t *k8_cache, const float *k_scale_cache, const uint8_t *k_cache8,
+                                       const uint8_t *v_cache8, const uint8_t *kv_exp, int scale_block,
+                                       const int32_t *block_table, int max_pages, int num_pages,
+                                       const int32_t *seq_lens, int max_seq_len, int B, int Hq, int Hkv, int D,
+                                       int HI, int dI, int k, float sm_scale, void *ws, size_t ws_bytes,
+                                       uint16_t *out, int32_t *idx_out, void *stream) {
+    const Range range(__func__);
+    dsa_status_t st = check_decode_common(block_table, max_pages, num_pages, seq_lens, max_seq_len, B);
+    if (st != DSA_OK) return st;
+    if (!dsa::indexer_shape_supported(HI, dI)) return DSA_ERR_UNSUPPORTED_SHAPE;
+    // the index rows are the workspace's or the caller's: any pointer stands for them here
+    st = check_kv8_attention(q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages, num_pages, seq_lens,
+                             q, B, Hq, Hkv, D, k, out);
+    if (st != DSA_OK) return st;
+    if (!dsa::topk_k_supported(k)) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (B == 0) return DSA_OK;
+    if (!q8 || !q_scale || !w || !k8_cache || !k_scale_cache) return DSA_ERR_INVALID_ARG;
+    if (!paged_keys_aligned(q8, k8_cache, k_scale_cache)) return DSA_ERR_INVALID_ARG;
+    const DecodeWs L = decode_ws_layout(B, max_seq_len, 1, 1, 0, k);
+    if (ws == nullptr || ws_bytes < L.attn_off || !aligned(ws, 16)) return DSA_ERR_WORKSPACE;
+    char *base = static_cast<char *>(ws);
+    float *scores = reinterpret_cast<float *>(base + L.scores_off);
+    int32_t *idx = idx_out ? idx_out : reinterpret_cast<int32_t *>(base + L.idx_off);
+    cudaStream_t s = as_stream(stream);
+    uint32_t *keyrange = reinterpret_cast<uint32_t *>(base + L.range_off);
+    cudaError_t e = cudaMemsetAsync(keyrange, 0xFF, L.preset_bytes, s);  // row key ranges
+    if (e != cudaSuccess) return cuda_status(e);
+    bool have_range = false;
+    if (max_seq_len > 0) {
+        e = dsa::launch_indexer_decode(q8, q_scale, w, k8_cache, k_scale_cache, block_table, max_pages, num_pages,
+                                       seq_lens, max_seq_len, B, HI, dI, scores, L.ld, s, keyrange, &have_range);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    e = dsa::launch_topk(scores, L.ld, 0, B, seq_lens, max_seq_len, k, idx, nullptr, base + L.topk_off,
+                         dsa::topk_workspace_bytes(B, max_seq_len, k), s, have_range ? keyrange : nullptr);
+    if (e != cudaSuccess) return cuda_status(e);
+    return cuda_status(dsa::launch_sparse_kv8(q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages,
+                                              num_pages, seq_lens, idx, nullptr, 0, 0, B, Hq, Hkv, D, k, sm_scale,
+                                              out, nullptr, s));
+}
+
+// ---------------------------------------------------------------------------
+// pages of a cache
+// ---------------------------------------------------------------------------
+
+static dsa_status_t check_page_bufs(void *const *bases, const size_t *page_bytes, int n_bufs) {
+    if (n_bufs < 0 || (n_bufs > 0 && (!bases || !page_bytes))) return DSA_ERR_INVALID_ARG;
+    if (n_bufs > dsa::kPagesMaxBufs) return DSA_ERR_UNSUPPORTED_SHAPE;
+    for (int i = 0; i < n_bufs; ++i) {
+        if (!bases[i] || page_bytes[i] == 0) return DSA_ERR_INVALID_ARG;
+        if (page_bytes[i] > (size_t(1) << 24)) return DSA_ERR_UNSUPPORTED_SHAPE;
+    }
+    return DSA_OK;
+}
+
+static dsa_status_t check_pool(int n, int n_slots, int max_pages, int num_pages) {
+    if (n < 0 || n_slots < 1 || max_pages < 1 || num_pages < 1) return DSA_ERR_INVALID_ARG;
+    if (n > dsa::kPagesMaxEntries || num_pages >= (1 << 25) || max_pages >= (1 << 25))
+        return DSA_ERR_UNSUPPORTED_SHAPE;
+    return DSA_OK;
+}
+
+dsa_status_t dsa_pages_extend(const int32_t *slots, const int32_t *new_lens, int n, int32_t *block_table,
+                              int n_slots, int max_pages, int32_t *seq_lens, int32_t *refcount, int num_pages,
+                              int32_t *status, void *stream) {
+    const Range range(__func__);
+    const dsa_status_t st = check_pool(n, n_slots, max_pages, num_pages);
+    if (st != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    if (!slots || !new_lens || !block_table || !seq_lens || !refcount || !status) return DSA_ERR_INVALID_ARG;
+    return cuda_status(dsa::launch_pages_extend(slots, new_lens, n, block_table, n_slots, max_pages, seq_lens,
+                                                refcount, num_pages, status, as_stream(stream)));
+}
+
+dsa_status_t dsa_pages_fork(void *const *bases, const size_t *page_bytes, int n_bufs, const int32_t *parents,
+                            const int32_t *children, int n, int32_t *block_table, int n_slots, int max_pages,
+                            int32_t *seq_lens, int32_t *refcount, int num_pages, int32_t *status, void *stream) {
+    const Range range(__func__);
+    dsa_status_t st = check_pool(n, n_slots, max_pages, num_pages);
+    if (st == DSA_OK) st = check_page_bufs(bases, page_bytes, n_bufs);
+    if (st != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    if (!parents || !children || !block_table || !seq_lens || !refcount || !status) return DSA_ERR_INVALID_ARG;
+    return cuda_status(dsa::launch_pages_fork(bases, page_bytes, n_bufs, parents, children, n, block_table, n_slots,
+                                              max_pages, seq_lens, refcount, num_pages, status, as_stream(stream)));
+}
+
+dsa_status_t dsa_pages_free(const int32_t *slots, int n, int32_t *block_table, int n_slots, int max_pages,
+                            int32_t *seq_lens, int32_t *refcount, int num_pages, void *stream) {
+    const Range range(__func__);
+    const dsa_status_t st = check_pool(n, n_slots, max_pages, num_pages);
+    if (st != DSA_OK) return st;
+    if (n == 0) return DSA_OK;
+    if (!slots || !block_table || !seq_lens || !refcount) return DSA_ERR_INVALID_ARG;
+    return cuda_status(dsa::launch_pages_free(slots, n, block_table, n_slots, max_pages, seq_lens, refcount,
+                                              num_pages, as_stream(stream)));
+}
+
+dsa_status_t dsa_pages_copy(void *const *bases, const size_t *page_bytes, int n_bufs, const int32_t *src,
+                            const int32_t *dst, int n, int num_pages, void *stream) {
+    const Range range(__func__);
+    if (n < 0 || num_pages < 1) return DSA_ERR_INVALID_ARG;
+    const dsa_status_t st = check_page_bufs(bases, page_bytes, n_bufs);
+    if (st != DSA_OK) return st;
+    if (n == 0 || n_bufs == 0) return DSA_OK;
+    if (!src || !dst) return DSA_ERR_INVALID_ARG;
+    return cuda_status(dsa::launch_pages_copy(bases, page_bytes, n_bufs, src, dst, n, num_pages, as_stream(stream)));
+}
+
+size_t dsa_pages_compact_workspace_size(int num_pages) {
+    return num_pages < 1 ? 0 : dsa::pages_compact_workspace_bytes(num_pages);
+}
+
+dsa_status_t dsa_pages_compact(void *const *bases, const size_t *page_bytes, int n_bufs, const int32_t *block_table,
+                               int32_t *block_table_out, int n_slots, int max_pages, const int32_t *seq_lens,
+                               const int32_t *refcount, int32_t *refcount_out, int num_pages, int32_t *page_map,
+                               int32_t *n_used, void *ws, size_t ws_bytes, void *stream) {
+    const Range range(__func__);
+    dsa_status_t st = check_pool(0, n_slots, max_pages, num_pages);
+    if (st == DSA_OK) st = check_page_bufs(bases, page_bytes, n_bufs);
+    if (st != DSA_OK) return st;
+    if (!block_table || !block_table_out || !seq_lens || !refcount || !refcount_out || !page_map || !n_used)
+        return DSA_ERR_INVALID_ARG;
+    if (ws == nullptr || ws_bytes < dsa::pages_compact_workspace_bytes(num_pages) || !aligned(ws, 16))
+        return DSA_ERR_WORKSPACE;
+    return cuda_status(dsa::launch_pages_compact(bases, page_bytes, n_bufs, block_table, block_table_out, n_slots,
+                                                 max_pages, seq_lens, refcount, refcount_out, num_pages, page_map,
+                                                 n_used, ws, as_stream(stream)));
+}
+
 dsa_status_t dsa_read_probe(const void *buf, size_t bytes, int reps, uint32_t *sink, void *stream) {
     const Range range(__func__);
     if (!buf || !sink || bytes == 0 || bytes % 16 != 0 || reps < 1) return DSA_ERR_INVALID_ARG;

@@ -1,0 +1,438 @@
+// attention_kv8.cu -- sparse GQA attention over the 8-bit paged cache.
+//
+// The formulas of attention.cu with K[s] = e4m3(k) * 2^ek and V[s] = e4m3(v)
+// * 2^ev, one pair of exponents per block of tokens and KV group.  In the
+// log2 domain, with c = sm_scale * log2(e), for a selected key i of a head:
+//     u_i = c * 2^ek_i * (q . k_i) + ev_i,     w_i = 2^(u_i - ref),
+//     O   = sum_i w_i v_i / sum_i w_i 2^-ev_i,
+//     lse = ln2 * (ref + log2 sum_i w_i 2^-ev_i).
+// Folding ev into the exponent bounds the weights that multiply V by the
+// largest product of weight and scale, so that they fit fp16 whatever the
+// scales; 2^-ev in the sum is exact.  ref moves only when a u exceeds it by
+// more than 15 (weights stay below 2^15 in fp16), and is then put 7 below the
+// largest u: nearly every block keeps it, and the check is one vote instead
+// of a maximum over the warp.
+//
+// e4m3 converts to fp16 without loss, and the products run on fp16 matrix
+// instructions with fp32 sums.  Q is bf16: each head's row is multiplied by
+// the power of two that puts its largest value into [2^14, 2^15), after which
+// fp16 holds every bf16 value that is not 2^-30 of the largest exactly; the
+// weights are rounded to fp16 (2^-11, half of what bf16 would cost twice
+// over), the sums are of the unrounded weights.
+//
+// Work unit: one warp owns 16 keys of a (query, KV group) pair at a time, all
+// G <= 8 heads at once (keys on the matrix M dimension, heads on N = 8).  The
+// selected rows go from global memory straight to the registers of the lane
+// that multiplies them: for S = K Q^T any permutation of the head dims is
+// allowed as long as Q has the same, so a lane takes 16 consecutive bytes;
+// for O^T = V^T P^T a lane takes the same 16 dims of keys 2t, 2t+1, 2t+8 and
+// 2t+9 and pairs their bytes with a byte permute.  There is no shared-memory
+// stage, no swizzle and no transpose, and each lane ends with 16 consecutive
+// dims of two heads.
+//
+// Pairs are split over several warps, and over the CTAs of a cluster, when
+// there are too few of them to fill the device; the partial results are
+// joined through shared memory (distributed shared memory across a cluster),
+// in a fixed order, in the same launch and without a workspace.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "kernels.h"
+#include "kv8.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace dsa {
+
+namespace {
+
+constexpr int kMaxWarps = 8;     // warps of a CTA
+constexpr int kMaxCluster = 8;   // CTAs of a cluster
+constexpr float kRefNone = -1e30f;
+
+struct Kv8Args {
+    const uint16_t *q;
+    const uint8_t *kc, *vc;
+    const uint16_t *exps;        // [pages, 64 / block, Hkv] pairs: K's byte low, V's high
+    const int32_t *block_table, *seq_lens, *idx, *cu;
+    int max_pages, num_pages, nseq, row_begin, n_rows, Hq, Hkv, k, block_shift, group_major;
+    float scale_log2;
+    uint16_t *out;
+    float *lse;
+};
+
+// The K and V bytes of 16 keys, as each lane multiplies them.
+template <int D>
+struct Tile {
+    uint32_t k[2][D / 64][4];    // keys gid, gid + 8: dims 64 j + 16 tig + 0..15
+    uint32_t v[4][D / 32];       // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: dims gid * D/8 + 0..
+};
+
+__device__ __forceinline__ void ldg_stream(uint32_t (&r)[4], const uint8_t *p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p));
+}
+__device__ __forceinline__ void ldg_stream(uint32_t (&r)[2], const uint8_t *p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+}
+
+// Issues the loads of keys half*16 .. +15 of the warp's 32: `row` holds, per
+// lane, the cache row of its key (-1: none, its bytes are taken as zero, so
+// that nothing of an unselected row reaches the products).
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D> &t, int row, int half, const uint8_t *kg, const uint8_t *vg,
+                                          uint32_t stride, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + gid + 8 * i);
+        const uint8_t *p = kg + (uint64_t)(uint32_t)r * stride + tig * 16;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) t.k[i][j][w] = 0u;
+            if (r >= 0) ldg_stream(t.k[i][j], p + j * 64);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + 2 * tig + (i & 1) + 8 * (i >> 1));
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) t.v[i][w] = 0u;
+        if (r >= 0) ldg_stream(t.v[i], vg + (uint64_t)(uint32_t)r * stride + gid * (D / 8));
+    }
+}
+
+// Running state of one warp: lane (gid, tig) holds heads 2 tig and 2 tig + 1;
+// o[m] are the products of one matrix instruction: dims gid * D/8 + 2 m
+// (o[m][0], o[m][1]) and + 2 m + 1 (o[m][2], o[m][3]) of the two heads.
+template <int D>
+struct Kv8State {
+    uint32_t q[D / 16][2];
+    float c[2];                  // c / (the power of two on Q's row), of the two heads
+    float o[D / 16][4];
+    float ref[2], l[2];
+};
+
+template <int D>
+__device__ __forceinline__ void init_state(Kv8State<D> &st, const uint16_t *qg, int G, float scale_log2, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+    uint4 raw[D / 64][2];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            raw[j][h] = make_uint4(0, 0, 0, 0);
+            if (gid < G)
+                raw[j][h] = __ldg(reinterpret_cast<const uint4 *>(qg + (size_t)gid * D + j * 64 + tig * 16) + h);
+            const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mx = max(mx, (w[i] << 16) & 0x7FFF0000u);
+                mx = max(mx, w[i] & 0x7FFF0000u);
+            }
+        }
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    // largest |q| of the head's row is 2^(ef - 127) * 1.x; the factor is
+    // 2^(141 - ef), its inverse 2^(ef - 141)
+    const int ef = min(max((int)(mx >> 23), 15), 254);
+    const float f = exp_byte_scale(268 - ef), inv = exp_byte_scale(ef - 14) * scale_log2;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
+            uint32_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                p[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+            st.q[j * 4 + 2 * h][0] = p[0];
+            st.q[j * 4 + 2 * h][1] = p[1];
+            st.q[j * 4 + 2 * h + 1][0] = p[2];
+            st.q[j * 4 + 2 * h + 1][1] = p[3];
+        }
+    st.c[0] = __shfl_sync(0xFFFFFFFFu, inv, tig * 8);       // head 2 tig is row gid = 2 tig
+    st.c[1] = __shfl_sync(0xFFFFFFFFu, inv, tig * 8 + 4);
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[m][i] = 0.f;
+    st.ref[0] = st.ref[1] = kRefNone;
+    st.l[0] = st.l[1] = 0.f;
+}
+
+// `meta` holds, per lane, its key's exponent bytes (K low, V high) or -1.
+template <int D>
+__device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, int meta, int half, int lane) {
+    const int gid = lane >> 2;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t x0 = t.k[0][j][w], x1 = t.k[1][j][w];
+            mma_f16_16816(s, e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
+                          e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)),
+                          st.q[j * 4 + w][0], st.q[j * 4 + w][1]);
+        }
+    const int m0 = __shfl_sync(0xFFFFFFFFu, meta, half * 16 + gid);
+    const int m8 = __shfl_sync(0xFFFFFFFFu, meta, half * 16 + gid + 8);
+    const float k0 = exp_byte_scale(m0 & 0xFF), k8 = exp_byte_scale(m8 & 0xFF);
+    const int e0 = (m0 >> 8) & 0xFF, e8 = (m8 >> 8) & 0xFF;
+    const float lv0 = m0 < 0 ? -INFINITY : (float)(e0 - 127), lv8 = m8 < 0 ? -INFINITY : (float)(e8 - 127);
+    const float iv0 = exp_byte_scale(254 - e0), iv8 = exp_byte_scale(254 - e8);
+    float u[4];
+    u[0] = m0 < 0 ? -INFINITY : fmaf(s[0], st.c[0] * k0, lv0);
+    u[1] = m0 < 0 ? -INFINITY : fmaf(s[1], st.c[1] * k0, lv0);
+    u[2] = m8 < 0 ? -INFINITY : fmaf(s[2], st.c[0] * k8, lv8);
+    u[3] = m8 < 0 ? -INFINITY : fmaf(s[3], st.c[1] * k8, lv8);
+    float mx[2] = {fmaxf(u[0], u[2]), fmaxf(u[1], u[3])};
+    if (__any_sync(0xFFFFFFFFu, mx[0] > st.ref[0] + 15.f || mx[1] > st.ref[1] + 15.f)) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], o));
+        }
+        float alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float ref = mx[i] > st.ref[i] + 15.f ? mx[i] - 7.f : st.ref[i];
+            alpha[i] = fast_exp2(st.ref[i] - ref);
+            st.ref[i] = ref;
+            st.l[i] *= alpha[i];
+        }
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) {
+            st.o[m][0] *= alpha[0];
+            st.o[m][1] *= alpha[1];
+            st.o[m][2] *= alpha[0];
+            st.o[m][3] *= alpha[1];
+        }
+    }
+    const float p0 = fast_exp2(u[0] - st.ref[0]), p1 = fast_exp2(u[1] - st.ref[1]);
+    const float p2 = fast_exp2(u[2] - st.ref[0]), p3 = fast_exp2(u[3] - st.ref[1]);
+    // an unselected key has no weight: its scale byte (255) must not make 0 * inf
+    st.l[0] += (m0 < 0 ? 0.f : p0 * iv0) + (m8 < 0 ? 0.f : p2 * iv8);
+    st.l[1] += (m0 < 0 ? 0.f : p1 * iv0) + (m8 < 0 ? 0.f : p3 * iv8);
+    const uint32_t b0 = movmatrix_trans(pack_f16x2(p0, p1));
+    const uint32_t b1 = movmatrix_trans(pack_f16x2(p2, p3));
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;   // two dims' bytes of two keys, by dim
+            const uint32_t x = __byte_perm(t.v[0][w], t.v[1][w], sel);
+            const uint32_t y = __byte_perm(t.v[2][w], t.v[3][w], sel);
+            mma_f16_16816(st.o[2 * w + h], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                          e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b0, b1);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMaxWarps * 32) sparse_kv8_kernel(const __grid_constant__ Kv8Args a) {
+    extern __shared__ __align__(16) float part[];   // [W][8][D] sums, [W][8][2] (ref, l), the CTA's [8][2]
+    const int lane = lane_id(), warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
+    const int pair = blockIdx.x / C;
+    const int r = a.group_major ? pair % a.n_rows : pair / a.Hkv;
+    const int g = a.group_major ? pair / a.n_rows : pair % a.Hkv;
+    const int G = a.Hq / a.Hkv;
+
+    // the query's sequence b and position t; rows outside every sequence are
+    // left as they are (the same answer in every CTA of a cluster)
+    int b, t;
+    if (a.cu == nullptr) {
+        b = r;
+        t = __ldg(a.seq_lens + b) - 1;
+    } else {
+        const int rr = a.row_begin + r;
+        if (rr < __ldg(a.cu) || rr >= __ldg(a.cu + a.nseq)) return;
+        b = warp_find_seq(a.nseq, rr, [&](int i) { return __ldg(a.cu + i); });
+        t = __ldg(a.seq_lens + b) - __ldg(a.cu + b + 1) + rr;
+    }
+    t = min(t, a.max_pages * kPage - 1);
+    const int n_vis = max(min(a.k, t + 1), 0);
+    const int32_t *idx_row = a.idx + (size_t)r * a.k;
+    const int32_t *bt = a.block_table + (size_t)b * a.max_pages;
+    const uint8_t *kg = a.kc + (size_t)g * D, *vg = a.vc + (size_t)g * D;
+    const uint32_t stride = (uint32_t)a.Hkv * D;
+
+    Kv8State<D> st;
+    init_state<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
+
+    // 32 keys a step, the pair's warps taking steps in turn
+    const int step0 = crank * W + warp, nw = C * W, steps = (n_vis + 31) / 32;
+    auto entry = [&](int step) {                    // the selected position, -1 if none
+        const int e = step * 32 + lane;
+        const int s = e < n_vis ? __ldg(idx_row + e) : -1;
+        return s <= t ? s : -1;
+    };
+    auto page_of = [&](int s) { return s >= 0 ? __ldg(bt + s / kPage) : -1; };
+    for (int step = step0; step < steps; step += nw) {
+        const int s = entry(step);
+        const int page = page_of(s);
+        int row = -1, meta = -1;
+        if (page >= 0 && page < a.num_pages) {
+            row = page * kPage + s % kPage;
+            meta = __ldg(a.exps + ((size_t)page * (kPage >> a.block_shift) + ((s % kPage) >> a.block_shift)) * a.Hkv + g);
+        }
+        Tile<D> t0;
+        load_tile<D>(t0, row, 0, kg, vg, stride, lane);
+        attend_tile<D>(st, t0, meta, 0, lane);
+        load_tile<D>(t0, row, 1, kg, vg, stride, lane);
+        attend_tile<D>(st, t0, meta, 1, lane);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        st.l[0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[0], o);
+        st.l[1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[1], o);
+    }
+    const int gid = lane >> 2, tig = lane & 3;
+    uint16_t *og = a.out + ((size_t)r * a.Hq + (size_t)g * G) * D;
+    float *lg = a.lse != nullptr ? a.lse + (size_t)r * a.Hq + (size_t)g * G : nullptr;
+    if (nw == 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int h = 2 * tig + i;
+            if (h >= G) continue;
+            const float inv = st.l[i] > 0.f ? 1.f / st.l[i] : 0.f;
+            uint32_t w[D / 16];
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) w[m] = pack_bf16x2(st.o[m][i] * inv, st.o[m][2 + i] * inv);
+            uint4 *dst = reinterpret_cast<uint4 *>(og + (size_t)h * D + gid * (D / 8));
+#pragma unroll
+            for (int m = 0; m < D / 64; ++m) dst[m] = make_uint4(w[4 * m], w[4 * m + 1], w[4 * m + 2], w[4 * m + 3]);
+            if (lg != nullptr && gid == 0) lg[h] = st.l[i] > 0.f ? (st.ref[i] + __log2f(st.l[i])) * kLn2 : -INFINITY;
+        }
+        return;
+    }
+    // join the warps' sums: within the CTA, then across the cluster
+    float *ml = part + (size_t)W * 8 * D, *cta_ml = ml + W * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)warp * 8 + 2 * tig + i) * D + gid * (D / 8));
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m)
+            dst[m] = make_float4(st.o[2 * m][i], st.o[2 * m][2 + i], st.o[2 * m + 1][i], st.o[2 * m + 1][2 + i]);
+        if (gid == 0) {
+            ml[(warp * 8 + 2 * tig + i) * 2] = st.ref[i];
+            ml[(warp * 8 + 2 * tig + i) * 2 + 1] = st.l[i];
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < G * (D / 2); e += blockDim.x) {
+        const int h = e / (D / 2), d = e % (D / 2) * 2;
+        float M = kRefNone;
+        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[(w * 8 + h) * 2]);
+        float L = 0.f, x = 0.f, y = 0.f;
+        for (int w = 0; w < W; ++w) {
+            const float f = fast_exp2(ml[(w * 8 + h) * 2] - M);
+            const float2 v = *reinterpret_cast<const float2 *>(part + ((size_t)w * 8 + h) * D + d);
+            L = fmaf(ml[(w * 8 + h) * 2 + 1], f, L);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+        }
+        if (C == 1) {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            *reinterpret_cast<uint32_t *>(og + (size_t)h * D + d) = pack_bf16x2(x * inv, y * inv);
+            if (lg != nullptr && d == 0) lg[h] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        } else {
+            *reinterpret_cast<float2 *>(part + (size_t)h * D + d) = make_float2(x, y);  // this thread's own place
+            if (d == 0) {
+                cta_ml[h * 2] = M;
+                cta_ml[h * 2 + 1] = L;
+            }
+        }
+    }
+    if (C == 1) return;
+    cluster.sync();
+    for (int e = crank * (int)blockDim.x + threadIdx.x; e < G * (D / 2); e += C * blockDim.x) {
+        const int h = e / (D / 2), d = e % (D / 2) * 2;
+        float ref[kMaxCluster], l[kMaxCluster];
+        float2 v[kMaxCluster];
+        float M = kRefNone;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            ref[c] = kRefNone;
+            l[c] = 0.f;
+            v[c] = make_float2(0.f, 0.f);
+            if (c < C) {
+                const float2 m = *reinterpret_cast<const float2 *>(cluster.map_shared_rank(cta_ml, c) + h * 2);
+                ref[c] = m.x;
+                l[c] = m.y;
+                v[c] = *reinterpret_cast<const float2 *>(cluster.map_shared_rank(part, c) + (size_t)h * D + d);
+            }
+            M = fmaxf(M, ref[c]);
+        }
+        float L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float f = fast_exp2(ref[c] - M);
+            L = fmaf(l[c], f, L);
+            x = fmaf(v[c].x, f, x);
+            y = fmaf(v[c].y, f, y);
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<uint32_t *>(og + (size_t)h * D + d) = pack_bf16x2(x * inv, y * inv);
+        if (lg != nullptr && d == 0) lg[h] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    }
+    cluster.sync();  // the cluster's shared memory is read until here
+}
+
+// How many warps share a pair, and in how many CTAs: enough that the pairs'
+// warps fill the device once, at most one per 32 keys.
+struct Split {
+    int warps, ctas;
+};
+Split split_of(int64_t pairs, int k, int slots) {
+    const int64_t most = (k + 31) / 32;
+    int64_t want = slots / pairs;
+    want = want < 1 ? 1 : (want > most ? most : want);
+    int ctas = 1;
+    while (ctas < kMaxCluster && want > (int64_t)ctas * kMaxWarps) ctas *= 2;
+    int64_t warps = want / ctas;
+    warps = warps < 1 ? 1 : (warps > kMaxWarps ? kMaxWarps : warps);
+    return {(int)warps, ctas};
+}
+
+template <int D>
+cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
+    constexpr int kSlots = 148 * 12;  // SMs x warps that the registers of a lane allow
+    const int64_t pairs = (int64_t)a.n_rows * a.Hkv;
+    const Split sp = split_of(pairs, a.k, kSlots);
+    const size_t smem = sp.warps * sp.ctas > 1 ? ((size_t)sp.warps * (8 * D + 16) + 16) * sizeof(float) : 0;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)sp.ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(pairs * sp.ctas));
+    cfg.blockDim = dim3(sp.warps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sparse_kv8_kernel<D>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sparse_kv8(const uint16_t *q, const uint8_t *k_cache8, const uint8_t *v_cache8,
+                              const uint8_t *kv_exp, int scale_block, const int32_t *block_table, int max_pages,
+                              int num_pages, const int32_t *seq_lens, const int32_t *idx, const int32_t *cu, int nseq,
+                              int row_begin, int n_rows, int Hq, int Hkv, int D, int k, float sm_scale, uint16_t *out,
+                              float *lse, cudaStream_t stream) {
+    if (n_rows == 0) return cudaSuccess;
+    const int shift = scale_block == 16 ? 4 : (scale_block == 32 ? 5 : 6);
+    const Kv8Args a{q, k_cache8, v_cache8, reinterpret_cast<const uint16_t *>(kv_exp), block_table, seq_lens, idx, cu,
+                    max_pages, num_pages, nseq, row_begin, n_rows, Hq, Hkv, k, shift, 0, sm_scale * kLog2e, out, lse};
+    return D == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace dsa

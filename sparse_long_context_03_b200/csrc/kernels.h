@@ -111,6 +111,42 @@ cudaError_t launch_sparse_decode_fixed_scratch(const uint16_t *q, const uint16_t
                                                int D, int k, float sm_scale, uint16_t *out, float *lse,
                                                cudaStream_t stream);
 
+// kv8_append.cu: K and V tokens into the 8-bit paged cache, with the indexer's
+// keys where k8 is given; cu NULL: one new token per sequence
+cudaError_t launch_kv8_append(const uint16_t *K, int64_t ld_k, const uint16_t *V, int64_t ld_v, const uint8_t *k8,
+                              const float *k_scale, const int32_t *cu, int nseq, int n_tokens,
+                              const int32_t *seq_lens, const int32_t *block_table, int max_pages, int num_pages,
+                              int Hkv, int D, int dI, int scale_block, uint8_t *k_cache8, uint8_t *v_cache8,
+                              uint8_t *kv_exp, uint8_t *k8_cache, float *k_scale_cache, cudaStream_t stream);
+
+// attention_kv8.cu: sparse GQA attention over the 8-bit paged cache; cu NULL:
+// row r is the newest token of sequence r, otherwise packed query rows
+cudaError_t launch_sparse_kv8(const uint16_t *q, const uint8_t *k_cache8, const uint8_t *v_cache8,
+                              const uint8_t *kv_exp, int scale_block, const int32_t *block_table, int max_pages,
+                              int num_pages, const int32_t *seq_lens, const int32_t *idx, const int32_t *cu, int nseq,
+                              int row_begin, int n_rows, int Hq, int Hkv, int D, int k, float sm_scale, uint16_t *out,
+                              float *lse, cudaStream_t stream);
+
+// pages.cu: the pages of a paged cache
+constexpr int kPagesMaxEntries = 1024;  // sequences of one call
+constexpr int kPagesMaxBufs = 8;        // cache buffers of one call
+cudaError_t launch_pages_extend(const int32_t *slots, const int32_t *new_lens, int n, int32_t *block_table,
+                                int n_slots, int max_pages, int32_t *seq_lens, int32_t *refcount, int num_pages,
+                                int32_t *status, cudaStream_t stream);
+cudaError_t launch_pages_fork(void *const *bases, const size_t *bytes, int n_bufs, const int32_t *parents,
+                              const int32_t *children, int n, int32_t *block_table, int n_slots, int max_pages,
+                              int32_t *seq_lens, int32_t *refcount, int num_pages, int32_t *status,
+                              cudaStream_t stream);
+cudaError_t launch_pages_free(const int32_t *slots, int n, int32_t *block_table, int n_slots, int max_pages,
+                              int32_t *seq_lens, int32_t *refcount, int num_pages, cudaStream_t stream);
+cudaError_t launch_pages_copy(void *const *bases, const size_t *bytes, int n_bufs, const int32_t *src,
+                              const int32_t *dst, int n, int num_pages, cudaStream_t stream);
+size_t pages_compact_workspace_bytes(int num_pages);
+cudaError_t launch_pages_compact(void *const *bases, const size_t *bytes, int n_bufs, const int32_t *table_in,
+                                 int32_t *table_out, int n_slots, int max_pages, const int32_t *seq_lens,
+                                 const int32_t *refs_in, int32_t *refs_out, int num_pages, int32_t *map,
+                                 int32_t *n_used, void *ws, cudaStream_t stream);
+
 // probe.cu: streaming 16-byte reads of a buffer, `reps` passes (bandwidth
 // measurement only)
 cudaError_t launch_read_probe(const void *buf, size_t bytes, int reps, uint32_t *sink, cudaStream_t stream);

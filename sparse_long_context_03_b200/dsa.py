@@ -57,6 +57,21 @@ _SIGNATURES = {
     "dsa_decode_attention_fixed_scratch_bytes": ([], _SZ),
     "dsa_sparse_gqa_decode_attention_noalloc": ([_P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _F,
                                                  _P, _P, _P], _I),
+    "dsa_kv8_append": ([_P, _I64, _P, _I64, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I,
+                        _P, _P, _P, _P, _P, _P], _I),
+    "dsa_sparse_gqa_decode_attention_kv8": ([_P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _F,
+                                             _P, _P, _P], _I),
+    "dsa_sparse_gqa_prefill_kv8": ([_P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
+                                    _P, _P, _P], _I),
+    "dsa_decode_kv8_workspace_size": ([_I, _I, _I], _SZ),
+    "dsa_sparse_gqa_decode_kv8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P, _I,
+                                   _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P, _P, _P], _I),
+    "dsa_pages_extend": ([_P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _P], _I),
+    "dsa_pages_fork": ([_P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _P], _I),
+    "dsa_pages_free": ([_P, _I, _P, _I, _I, _P, _P, _I, _P], _I),
+    "dsa_pages_copy": ([_P, _P, _I, _P, _P, _I, _I, _P], _I),
+    "dsa_pages_compact_workspace_size": ([_I], _SZ),
+    "dsa_pages_compact": ([_P, _P, _I, _P, _P, _I, _I, _P, _P, _P, _I, _P, _P, _P, _SZ, _P], _I),
     "dsa_read_probe": ([_P, _SZ, _I, _P, _P], _I),
 }
 
@@ -473,6 +488,365 @@ def sparse_gqa_decode_attention_noalloc(q, k_cache, v_cache, block_table, seq_le
                                                          _ptr(idx), B, Hq, Hkv, D, int(k), float(sm_scale),
                                                          _ptr(out), _ptr(lse), _stream(stream)),
            "dsa_sparse_gqa_decode_attention_noalloc")
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit KV cache
+# ---------------------------------------------------------------------------
+
+KV8_EXP_MIN = 87  # the least scale exponent byte: 2^-40
+
+
+def _shaped(t, dtype, shape, name, device):
+    """``t`` is a dense tensor of this type and shape on ``device``."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.device
+
+
+def _call(name, device, stream, *args):
+    """The entry point, on ``device`` (made current if it is not) and on the
+    given stream or that device's current one."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), name)
+
+
+def _kv8_cache(k_cache8, v_cache8, kv_exp):
+    """Checks the three buffers of an 8-bit cache; (num_pages, Hkv, D, scale_block)."""
+    device = _device_of(k_cache8, "k_cache8")
+    if k_cache8.dim() != 4 or k_cache8.shape[1] != PAGE_SIZE:
+        raise ValueError(f"k_cache8: expected [num_pages, {PAGE_SIZE}, Hkv, D], got {tuple(k_cache8.shape)}")
+    P, _, Hkv, D = k_cache8.shape
+    _shaped(k_cache8, torch.uint8, (P, PAGE_SIZE, Hkv, D), "k_cache8", device)
+    _shaped(v_cache8, torch.uint8, (P, PAGE_SIZE, Hkv, D), "v_cache8", device)
+    parts = kv_exp.shape[1] if kv_exp.dim() == 4 else 0
+    if parts not in (1, 2, 4):
+        raise ValueError(f"kv_exp: expected [num_pages, 1, 2 or 4, Hkv, 2], got {tuple(kv_exp.shape)}")
+    _shaped(kv_exp, torch.uint8, (P, parts, Hkv, 2), "kv_exp", device)
+    return P, Hkv, D, PAGE_SIZE // parts
+
+
+def _token_rows(t, n, Hkv, D, name, device):
+    """Checks [n, Hkv, D] bf16 rows that may lie apart; the distance in elements."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (n, Hkv, D):
+        raise ValueError(f"{name}: expected shape {(n, Hkv, D)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+    if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's [Hkv, D] values must be contiguous")
+    return t.stride(0) if n > 1 else Hkv * D
+
+
+def _table(block_table, seq_lens, n, device):
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: expected 2 dims, got shape {tuple(block_table.shape)}")
+    _shaped(block_table, torch.int32, (n, block_table.shape[1]), "block_table", device)
+    _shaped(seq_lens, torch.int32, (n,), "seq_lens", device)
+    return block_table.shape[1]
+
+
+def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqlens=None, k8=None, k_scale=None,
+               k8_cache=None, k_scale_cache=None, stream=None):
+    """dsa_kv8_append: new tokens' K and V [n, Hkv, D] bf16 (rows may be parts
+    of wider ones) into the 8-bit cache, as the last tokens of sequences whose
+    seq_lens [nseq] count them already.  cu_seqlens int32 [nseq+1] for packed
+    new tokens, None for one per sequence.  k8 [n, dI] uint8 and k_scale [n]
+    float32, with their caches, add the indexer's keys."""
+    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
+    device = k_cache8.device
+    n, nseq = K.shape[0], seq_lens.shape[0]
+    ld_k = _token_rows(K, n, Hkv, D, "K", device)
+    ld_v = _token_rows(V, n, Hkv, D, "V", device)
+    max_pages = _table(block_table, seq_lens, nseq, device)
+    if cu_seqlens is not None:
+        _shaped(cu_seqlens, torch.int32, (nseq + 1,), "cu_seqlens", device)
+    elif n != nseq:
+        raise ValueError(f"K: expected one token for each of {nseq} sequences, got {n}")
+    dI = 0
+    if k8 is not None:
+        if k_scale is None or k8_cache is None or k_scale_cache is None:
+            raise ValueError("k8, k_scale, k8_cache and k_scale_cache go together")
+        dI = k8.shape[-1]
+        _shaped(k8, torch.uint8, (n, dI), "k8", device)
+        _shaped(k_scale, torch.float32, (n,), "k_scale", device)
+        _shaped(k8_cache, torch.uint8, (P, PAGE_SIZE, dI), "k8_cache", device)
+        _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
+    elif k_scale is not None or k8_cache is not None or k_scale_cache is not None:
+        raise ValueError("k8, k_scale, k8_cache and k_scale_cache go together")
+    _call("dsa_kv8_append", device, stream, _ptr(K), ld_k, _ptr(V), ld_v, _ptr(k8), _ptr(k_scale), _ptr(cu_seqlens),
+          nseq, n, _ptr(seq_lens), _ptr(block_table), max_pages, P, Hkv, D, dI, block, _ptr(k_cache8),
+          _ptr(v_cache8), _ptr(kv_exp), _ptr(k8_cache), _ptr(k_scale_cache))
+
+
+def _kv8_rows(q, idx, k, out, lse, Hkv, D, device):
+    """Checks the query-side tensors of an attention call; (rows, Hq)."""
+    if q.dim() != 3:
+        raise ValueError(f"q: expected 3 dims, got shape {tuple(q.shape)}")
+    n, Hq = q.shape[0], q.shape[1]
+    _shaped(q, torch.bfloat16, (n, Hq, D), "q", device)
+    if idx is not None:
+        _shaped(idx, torch.int32, (n, k), "idx", device)
+    _shaped(out, torch.bfloat16, (n, Hq, D), "out", device)
+    if lse is not None:
+        _shaped(lse, torch.float32, (n, Hq), "lse", device)
+    return n, Hq
+
+
+def sparse_gqa_decode_attention_kv8(q, k_cache8, v_cache8, kv_exp, block_table, seq_lens, idx, k, sm_scale, out,
+                                    lse=None, stream=None):
+    """dsa_sparse_gqa_decode_attention_kv8: attention of each sequence's newest
+    token over its selected rows idx [B, k] of the 8-bit cache."""
+    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
+    device = k_cache8.device
+    B, Hq = _kv8_rows(q, idx, int(k), out, lse, Hkv, D, device)
+    max_pages = _table(block_table, seq_lens, B, device)
+    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream, _ptr(q), _ptr(k_cache8), _ptr(v_cache8),
+          _ptr(kv_exp), block, _ptr(block_table), max_pages, P, _ptr(seq_lens), _ptr(idx), B, Hq, Hkv, D, int(k),
+          float(sm_scale), _ptr(out), _ptr(lse))
+
+
+def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens, idx, cu_seqlens, row_begin, n_rows,
+                           k, sm_scale, O, lse=None, stream=None):
+    """dsa_sparse_gqa_prefill_kv8: attention of packed query rows [row_begin,
+    row_begin+n_rows), the last tokens of their cached sequences, over their
+    selected positions in the 8-bit cache.  Q, O, idx and lse hold these rows."""
+    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
+    device = k_cache8.device
+    n, Hq = _kv8_rows(Q, idx, int(k), O, lse, Hkv, D, device)
+    if n != int(n_rows):
+        raise ValueError(f"Q: expected {int(n_rows)} rows, got {n}")
+    nseq = seq_lens.shape[0]
+    max_pages = _table(block_table, seq_lens, nseq, device)
+    _shaped(cu_seqlens, torch.int32, (nseq + 1,), "cu_seqlens", device)
+    _call("dsa_sparse_gqa_prefill_kv8", device, stream, _ptr(Q), _ptr(k_cache8), _ptr(v_cache8), _ptr(kv_exp), block,
+          _ptr(block_table), max_pages, P, _ptr(seq_lens), _ptr(idx), _ptr(cu_seqlens), nseq, int(row_begin), n, Hq,
+          Hkv, D, int(k), float(sm_scale), _ptr(O), _ptr(lse))
+
+
+def decode_kv8_workspace_size(B, max_seq_len, k) -> int:
+    return int(lib().dsa_decode_kv8_workspace_size(int(B), int(max_seq_len), int(k)))
+
+
+def sparse_gqa_decode_kv8(q, q8, q_scale, w, k8_cache, k_scale_cache, k_cache8, v_cache8, kv_exp, block_table,
+                          seq_lens, max_seq_len, k, sm_scale, ws, out, idx_out=None, stream=None):
+    """dsa_sparse_gqa_decode_kv8: indexer -> top-k -> attention over the 8-bit
+    cache, for one new token per sequence.  ``ws`` is a uint8 CUDA tensor of
+    decode_kv8_workspace_size(...) bytes or more."""
+    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
+    device = k_cache8.device
+    B, Hq = _kv8_rows(q, idx_out, int(k), out, None, Hkv, D, device)
+    max_pages = _table(block_table, seq_lens, B, device)
+    if q8.dim() != 3:
+        raise ValueError(f"q8: expected 3 dims, got shape {tuple(q8.shape)}")
+    HI, dI = q8.shape[1], q8.shape[2]
+    _shaped(q8, torch.uint8, (B, HI, dI), "q8", device)
+    _shaped(q_scale, torch.float32, (B,), "q_scale", device)
+    _shaped(w, torch.float32, (B, HI), "w", device)
+    _shaped(k8_cache, torch.uint8, (P, PAGE_SIZE, dI), "k8_cache", device)
+    _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
+    if _device_of(ws, "ws") != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {device}")
+    _call("dsa_sparse_gqa_decode_kv8", device, stream, _ptr(q), _ptr(q8), _ptr(q_scale), _ptr(w), _ptr(k8_cache),
+          _ptr(k_scale_cache), _ptr(k_cache8), _ptr(v_cache8), _ptr(kv_exp), block, _ptr(block_table), max_pages, P,
+          _ptr(seq_lens), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k), float(sm_scale), _ptr(ws),
+          ws.numel() * ws.element_size(), _ptr(out), _ptr(idx_out))
+
+
+# ---------------------------------------------------------------------------
+# pages of a cache
+# ---------------------------------------------------------------------------
+
+def _page_bufs(bufs, num_pages, device):
+    """Host arrays of the buffers' addresses and page sizes; each buffer is a
+    dense tensor [num_pages, ...]."""
+    n = len(bufs)
+    bases, sizes = (_P * n)(), (_SZ * n)()
+    for i, t in enumerate(bufs):
+        if t.device != device:
+            raise ValueError(f"bufs[{i}]: expected on {device}, got {t.device}")
+        if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
+            raise ValueError(f"bufs[{i}]: expected a contiguous tensor of {num_pages} pages, got {tuple(t.shape)}")
+        bases[i] = t.data_ptr()
+        sizes[i] = t.numel() // num_pages * t.element_size()
+    return bases, sizes, n
+
+
+def _pool(block_table, seq_lens, refcount):
+    """Checks a pool's state; (device, n_slots, max_pages, num_pages)."""
+    device = _device_of(block_table, "block_table")
+    max_pages = _table(block_table, seq_lens, block_table.shape[0], device)
+    if refcount.dim() != 1:
+        raise ValueError(f"refcount: expected 1 dim, got shape {tuple(refcount.shape)}")
+    _shaped(refcount, torch.int32, (refcount.shape[0],), "refcount", device)
+    return device, block_table.shape[0], max_pages, refcount.shape[0]
+
+
+def _entries(device, **lists):
+    n = len(next(iter(lists.values())))
+    for name, t in lists.items():
+        _shaped(t, torch.int32, (n,), name, device)
+    return n
+
+
+def pages_extend(slots, new_lens, block_table, seq_lens, refcount, status, stream=None):
+    """dsa_pages_extend: sequence slots[i] grows to new_lens[i] tokens and gets
+    the pages that takes; status[i] = 0, or 1 (no pages left) or 2 (refused)."""
+    device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
+    n = _entries(device, slots=slots, new_lens=new_lens, status=status)
+    _call("dsa_pages_extend", device, stream, _ptr(slots), _ptr(new_lens), n, _ptr(block_table), n_slots, max_pages,
+          _ptr(seq_lens), _ptr(refcount), P, _ptr(status))
+
+
+def pages_fork(bufs, parents, children, block_table, seq_lens, refcount, status, stream=None):
+    """dsa_pages_fork: the empty slot children[i] becomes a copy of sequence
+    parents[i]: full pages shared, a partly filled last page copied in every
+    buffer of ``bufs`` (tensors [num_pages, ...]); status as in pages_extend."""
+    device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
+    n = _entries(device, parents=parents, children=children, status=status)
+    bases, sizes, n_bufs = _page_bufs(bufs, P, device)
+    _call("dsa_pages_fork", device, stream, bases, sizes, n_bufs, _ptr(parents), _ptr(children), n,
+          _ptr(block_table), n_slots, max_pages, _ptr(seq_lens), _ptr(refcount), P, _ptr(status))
+
+
+def pages_free(slots, block_table, seq_lens, refcount, stream=None):
+    """dsa_pages_free: the sequences in ``slots`` become empty and pages that no
+    other sequence holds become free."""
+    device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
+    n = _entries(device, slots=slots)
+    _call("dsa_pages_free", device, stream, _ptr(slots), n, _ptr(block_table), n_slots, max_pages, _ptr(seq_lens),
+          _ptr(refcount), P)
+
+
+def pages_copy(bufs, src, dst, stream=None):
+    """dsa_pages_copy: page src[i] to page dst[i] in every buffer of ``bufs``
+    (tensors [num_pages, ...])."""
+    if not bufs:
+        raise ValueError("bufs: expected at least one buffer")
+    device = _device_of(bufs[0], "bufs[0]")
+    if bufs[0].dim() < 1:
+        raise ValueError("bufs[0]: expected [num_pages, ...]")
+    P = bufs[0].shape[0]
+    n = _entries(device, src=src, dst=dst)
+    bases, sizes, n_bufs = _page_bufs(bufs, P, device)
+    _call("dsa_pages_copy", device, stream, bases, sizes, n_bufs, _ptr(src), _ptr(dst), n, P)
+
+
+def pages_compact_workspace_size(num_pages) -> int:
+    return int(lib().dsa_pages_compact_workspace_size(int(num_pages)))
+
+
+def pages_compact(bufs, block_table, seq_lens, refcount, page_map, n_used, ws, block_table_out=None,
+                  refcount_out=None, stream=None):
+    """dsa_pages_compact: the pages in use come to the lowest ids, in every
+    buffer of ``bufs``; page_map [num_pages] int32 receives the new ids (-1:
+    free), n_used [1] int32 their number.  The table and the counts change in
+    place unless other tensors are given for them."""
+    device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
+    table_out = block_table if block_table_out is None else block_table_out
+    refs_out = refcount if refcount_out is None else refcount_out
+    _shaped(table_out, torch.int32, (n_slots, max_pages), "block_table_out", device)
+    _shaped(refs_out, torch.int32, (P,), "refcount_out", device)
+    _shaped(page_map, torch.int32, (P,), "page_map", device)
+    _shaped(n_used, torch.int32, (1,), "n_used", device)
+    if _device_of(ws, "ws") != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {device}")
+    bases, sizes, n_bufs = _page_bufs(bufs, P, device)
+    _call("dsa_pages_compact", device, stream, bases, sizes, n_bufs, _ptr(block_table), _ptr(table_out), n_slots,
+          max_pages, _ptr(seq_lens), _ptr(refcount), _ptr(refs_out), P, _ptr(page_map), _ptr(n_used), _ptr(ws),
+          ws.numel() * ws.element_size())
+
+
+class KV8Cache:
+    """Buffers of an 8-bit paged cache and of its pool of pages: K and V
+    (``k``, ``v``, ``exp``), the indexer's keys (``k8``, ``k_scale``; with dI),
+    and the pool's ``block_table``, ``seq_lens`` and ``refcount``.
+
+    The methods call the functions of this module on the current stream.
+    ``slots`` is an int32 CUDA tensor of the sequences that take part, in the
+    order of the batch; None means every slot in order."""
+
+    def __init__(self, num_pages, n_slots, max_pages, Hkv, D, dI=None, scale_block=64, device="cuda"):
+        if scale_block not in (16, 32, 64):
+            raise ValueError(f"scale_block: expected 16, 32 or 64, got {scale_block}")
+        e8 = dict(dtype=torch.uint8, device=device)
+        e32 = dict(dtype=torch.int32, device=device)
+        self.k = torch.zeros(num_pages, PAGE_SIZE, Hkv, D, **e8)
+        self.v = torch.zeros(num_pages, PAGE_SIZE, Hkv, D, **e8)
+        self.exp = torch.full((num_pages, PAGE_SIZE // scale_block, Hkv, 2), KV8_EXP_MIN, **e8)
+        self.k8 = torch.zeros(num_pages, PAGE_SIZE, dI, **e8) if dI else None
+        self.k_scale = torch.ones(num_pages, PAGE_SIZE, dtype=torch.float32, device=device) if dI else None
+        self.block_table = torch.full((n_slots, max_pages), -1, **e32)
+        self.seq_lens = torch.zeros(n_slots, **e32)
+        self.refcount = torch.zeros(num_pages, **e32)
+        self.bufs = [t for t in (self.k, self.v, self.exp, self.k8, self.k_scale) if t is not None]
+
+    def _rows(self, slots):
+        if slots is None:
+            return self.block_table, self.seq_lens
+        return self.block_table.index_select(0, slots), self.seq_lens.index_select(0, slots)
+
+    def extend(self, slots, new_lens):
+        """pages_extend; the status tensor."""
+        status = torch.empty_like(slots)
+        pages_extend(slots, new_lens, self.block_table, self.seq_lens, self.refcount, status)
+        return status
+
+    def fork(self, parents, children):
+        """pages_fork; the status tensor."""
+        status = torch.empty_like(children)
+        pages_fork(self.bufs, parents, children, self.block_table, self.seq_lens, self.refcount, status)
+        return status
+
+    def free(self, slots):
+        pages_free(slots, self.block_table, self.seq_lens, self.refcount)
+
+    def compact(self):
+        """pages_compact in place; (page_map, n_used)."""
+        page_map = torch.empty_like(self.refcount)
+        n_used = torch.empty(1, dtype=torch.int32, device=self.refcount.device)
+        ws = torch.empty(pages_compact_workspace_size(len(self.refcount)), dtype=torch.uint8,
+                         device=self.refcount.device)
+        pages_compact(self.bufs, self.block_table, self.seq_lens, self.refcount, page_map, n_used, ws)
+        return page_map, n_used
+
+    def append(self, K, V, cu_seqlens=None, k8=None, k_scale=None, slots=None):
+        """kv8_append of the last tokens of the sequences (extend comes first)."""
+        table, lens = self._rows(slots)
+        kv8_append(K, V, self.k, self.v, self.exp, table, lens, cu_seqlens, k8, k_scale,
+                   self.k8 if k8 is not None else None, self.k_scale if k8 is not None else None)
+
+    def prefill(self, Q, idx, cu_seqlens, O, sm_scale=None, lse=None, slots=None):
+        """sparse_gqa_prefill_kv8 of all packed query rows."""
+        table, lens = self._rows(slots)
+        scale = 1.0 / math.sqrt(Q.shape[2]) if sm_scale is None else sm_scale
+        sparse_gqa_prefill_kv8(Q, self.k, self.v, self.exp, table, lens, idx, cu_seqlens, 0, Q.shape[0],
+                               idx.shape[1], scale, O, lse)
+
+    def decode(self, q, q8, q_scale, w, max_seq_len, k, ws, out, sm_scale=None, idx_out=None, slots=None):
+        """sparse_gqa_decode_kv8 of one new token per sequence."""
+        if self.k8 is None:
+            raise ValueError("the cache holds no indexer keys (dI)")
+        table, lens = self._rows(slots)
+        scale = 1.0 / math.sqrt(q.shape[2]) if sm_scale is None else sm_scale
+        sparse_gqa_decode_kv8(q, q8, q_scale, w, self.k8, self.k_scale, self.k, self.v, self.exp, table, lens,
+                              max_seq_len, k, scale, ws, out, idx_out)
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,304 @@
+"""The pages of a cache on the GPU against the plain pool (kv8_reference.Pool):
+tables, lengths, counts, statuses and bytes are equal after every call."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_reference as ref
+from sparse_long_context_03_b200 import dsa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x, np.int32), device=DEV)
+
+
+class Both:
+    """A plain pool and one on the GPU, called alike and compared after each call."""
+
+    def __init__(self, P, slots, max_pages, shapes, seed):
+        rng = np.random.default_rng(seed)
+        self.bufs = [rng.integers(0, 256, (P,) + s).astype(np.uint8) for s in shapes]
+        self.pool = ref.Pool(P, slots, max_pages, [b.copy() for b in self.bufs])
+        self.g = [torch.from_numpy(b).to(DEV) for b in self.bufs]
+        self.state = [i32(x) for x in (self.pool.table, self.pool.lens, self.pool.refs)]
+
+    def same(self, status=None, want=None):
+        torch.cuda.synchronize()
+        for name, a, b in zip(("table", "lens", "refs"), self.state, (self.pool.table, self.pool.lens, self.pool.refs)):
+            assert np.array_equal(a.cpu().numpy(), b), name
+        if status is not None:
+            assert np.array_equal(status.cpu().numpy(), want), "status"
+        for i, (a, b) in enumerate(zip(self.g, self.pool.bufs)):
+            assert np.array_equal(a.cpu().numpy(), b), f"buffer {i}"
+
+    def extend(self, slots, lens):
+        st = torch.full((len(slots),), 99, dtype=torch.int32, device=DEV)
+        dsa.pages_extend(i32(slots), i32(lens), *self.state, st)
+        self.same(st, want := self.pool.extend(slots, lens))
+        return want
+
+    def fork(self, parents, children):
+        st = torch.full((len(parents),), 99, dtype=torch.int32, device=DEV)
+        dsa.pages_fork(self.g, i32(parents), i32(children), *self.state, st)
+        self.same(st, want := self.pool.fork(parents, children))
+        return want
+
+    def free(self, slots):
+        dsa.pages_free(i32(slots), *self.state)
+        self.pool.free(slots)
+        self.same()
+
+    def compact(self, in_place=True):
+        P = len(self.pool.refs)
+        pmap, used = torch.empty(P, dtype=torch.int32, device=DEV), i32([0])
+        ws = torch.empty(dsa.pages_compact_workspace_size(P), dtype=torch.uint8, device=DEV)
+        kw = {}
+        if not in_place:
+            before = [t.clone() for t in self.state]
+            kw = dict(block_table_out=torch.full_like(self.state[0], 55), refcount_out=torch.full_like(self.state[2], 55))
+        dsa.pages_compact(self.g, *self.state, pmap, used, ws, **kw)
+        if kw:
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(before, self.state))
+            self.state = [kw["block_table_out"], self.state[1], kw["refcount_out"]]
+        m, n = self.pool.compact()
+        self.same()
+        assert np.array_equal(pmap.cpu().numpy(), m) and int(used) == n
+
+
+# page sizes of 16-byte units and of 8, 4, 2 and 1 byte units, larger and smaller than a piece
+SHAPES = [(64, 40), (24,), (4, 3), (6,), (13,), (16,), (5, 4096)]
+
+
+@pytest.mark.parametrize("P", [37, 700])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_random_calls(P, seed):
+    rng = np.random.default_rng(seed * 100 + P)
+    slots, max_pages = 12, 9
+    b = Both(P, slots, max_pages, SHAPES, seed)
+    for _ in range(60):
+        op = rng.integers(5)
+        n = int(rng.integers(1, 9))
+        s = rng.integers(-1, slots + 1, n)      # out of range and the same one twice among them
+        if op <= 1:
+            at = np.clip(s, 0, slots - 1)
+            b.extend(s, b.pool.lens[at] + rng.integers(-3, 200, n))
+        elif op == 2:
+            b.fork(rng.integers(0, slots, n), s)
+        elif op == 3:
+            b.free(s[:3])
+        else:
+            b.compact(in_place=bool(rng.integers(2)))
+
+
+def test_statuses():
+    b = Both(4, 6, 3, [(16,)], 1)
+    assert list(b.extend([0, 1, 0, 6, -1, 2], [100, 0, 128, 5, 5, 193])) == [0, 0, 2, 2, 2, 2]
+    # two pages left: the second entry is refused, then every one that needs a page
+    assert list(b.extend([2, 3, 4, 0, 5], [64, 128, 64, 128, 0])) == [0, 1, 1, 0, 0]
+    assert list(b.extend([0], [127])) == [2]                       # never shorter
+    assert list(b.fork([0, 2, 0, 3], [1, 2, 9, 3])) == [0, 2, 2, 0]  # slot 2 is not empty, 9 is none, 3 is empty itself
+    assert list(b.extend([4], [33])) == [0]
+    assert list(b.fork([4, 0, 4], [3, 5, 3])) == [1, 0, 2]           # no page for a partly filled last one
+
+
+def test_fork_shares_and_frees_in_any_order():
+    b = Both(300, 40, 20, SHAPES[:3], 2)
+    b.extend([0, 1, 2], [1000, 64, 130])
+    b.fork([0] * 10 + [1] * 5 + [2] * 5, np.arange(10, 30))
+    b.fork([12, 29], [30, 31])                 # forks of forks
+    b.extend(np.arange(10, 30), b.pool.lens[10:30] + 70)
+    b.free([0, 0, 1, 2, 2, 0])                 # the same slot several times
+    b.free(np.arange(10, 32))
+    assert b.pool.refs.sum() == 0
+
+
+@pytest.mark.parametrize("P", [16384, 16385, 200001])
+def test_large_pools(P):
+    # over the size from which several CTAs share the counts; the free pages at
+    # the far end, and a pool with none left
+    rng = np.random.default_rng(P)
+    slots, max_pages = 1024, 256
+    b = Both(P, slots, max_pages, [(16,)], 3)
+    b.pool.refs[:] = rng.random(P) < 0.7
+    b.pool.refs[: P // 2] = 1
+    b.pool.refs[-1] = 0
+    b.state[2].copy_(i32(b.pool.refs))
+    n_free = int((b.pool.refs == 0).sum())
+    want = rng.integers(0, 64 * max(n_free // 1000, 2), slots)
+    b.extend(rng.permutation(slots), want)
+    b.extend(rng.permutation(slots), np.minimum(b.pool.lens.max() + 700, 64 * max_pages) + np.zeros(slots, int))
+    b.fork(rng.integers(0, 10, 20), rng.integers(0, slots, 20))
+    b.free(rng.permutation(slots)[:1000])
+    b.compact()
+
+
+def test_extend_grants_every_last_page():
+    b = Both(20000, 2, 20000, [(16,)], 4)
+    assert list(b.extend([1], [64 * 20000])) == [0]
+    assert list(b.extend([0], [1])) == [1]
+    b.free([1])
+    assert list(b.extend([0], [64 * 20000 - 1])) == [0]
+
+
+def test_counts_below_zero_are_never_granted():
+    b = Both(50, 3, 60, [(16,)], 5)
+    b.pool.refs[[0, 3, 49]] = -1
+    b.state[2].copy_(i32(b.pool.refs))
+    assert list(b.extend([0], [64 * 48])) == [1]
+    assert list(b.extend([0], [64 * 47])) == [0]
+    b.free([0])
+    assert list(b.pool.refs[[0, 3, 49]]) == [-1, -1, -1]
+
+
+@pytest.mark.parametrize("P", [40, 5000])
+def test_compact_of_empty_full_and_packed_pools(P):
+    b = Both(P, 4, P, [(64,), (3,)], 6)
+    b.compact()
+    b.extend([0], [64 * P])
+    b.compact()
+    b.free([0])
+    b.extend([1, 2, 3], [64 * (P // 4), 1, 64 * (P // 2)])
+    b.compact(in_place=False)
+    b.free([1])
+    b.compact()
+    b.compact()
+
+
+@pytest.mark.parametrize("n", [1, 500])
+def test_copy(n):
+    rng = np.random.default_rng(n)
+    P = 1200
+    bufs = [rng.integers(0, 256, (P,) + s).astype(np.uint8) for s in SHAPES]
+    both = rng.permutation(P)
+    src, dst = both[:n].copy(), both[n:2 * n].copy()
+    if n > 10:
+        src[3] = src[4]              # one page to two places
+        dst[5], src[6], dst[7] = P, -1, -9   # skipped
+        dst[8] = src[8]
+    g = [torch.from_numpy(b).to(DEV) for b in bufs]
+    g.append(torch.arange(P * 6, device=DEV, dtype=torch.float32).view(P, 6))
+    want = [t.cpu().numpy().copy() for t in g]
+    for s, d in zip(src, dst):
+        if 0 <= s < P and 0 <= d < P:
+            for w in want:
+                w[d] = w[s]
+    dsa.pages_copy(g, i32(src), i32(dst))
+    torch.cuda.synchronize()
+    for a, b in zip(g, want):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_copy_of_buffers_off_their_alignment():
+    # a buffer that starts 4 bytes past a 16-byte boundary moves in smaller units
+    P = 30
+    base = torch.randint(0, 256, (P * 48 + 4,), dtype=torch.uint8, device=DEV)
+    t = base[4:].view(P, 48)
+    want = t.cpu().numpy().copy()
+    want[[7, 9]] = want[[1, 2]]
+    dsa.pages_copy([t], i32([1, 2]), i32([7, 9]))
+    torch.cuda.synchronize()
+    assert np.array_equal(t.cpu().numpy(), want)
+
+
+def test_copy_behind_four_gigabytes():
+    P, size = 70000, 65536
+    t = torch.zeros(P, size, dtype=torch.uint8, device=DEV)
+    t[P - 1] = 7
+    t[65537, ::2] = 9
+    dsa.pages_copy([t], i32([P - 1, 65537]), i32([3, P - 2]))
+    torch.cuda.synchronize()
+    assert bool((t[3] == 7).all()) and bool((t[P - 2] == t[65537]).all())
+
+
+def test_captured_calls_replay():
+    b = Both(400, 10, 30, [(64, 8)], 7)
+    slots, to, st = i32([0, 1, 2]), i32([0, 0, 0]), i32([9, 9, 9])
+    par, chi, st2 = i32([0, 1]), i32([5, 6]), i32([9, 9])
+    dsa.pages_free(chi, *b.state)      # every kernel has run once before the capture
+    dsa.pages_extend(slots, to, *b.state, st)
+    dsa.pages_fork(b.g, par, chi, *b.state, st2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dsa.pages_free(chi, *b.state)
+        dsa.pages_extend(slots, to, *b.state, st)
+        dsa.pages_fork(b.g, par, chi, *b.state, st2)
+    lens = np.zeros(3, int)
+    rng = np.random.default_rng(0)
+    for _ in range(12):
+        lens = lens + rng.integers(0, 150, 3)
+        to.copy_(i32(lens))
+        g.replay()
+        b.pool.free([5, 6])
+        w1 = b.pool.extend([0, 1, 2], lens)
+        w2 = b.pool.fork([0, 1], [5, 6])
+        b.same(st, w1)
+        assert np.array_equal(st2.cpu().numpy(), w2)
+
+
+def test_a_serving_run_of_them_together():
+    """Prompts appended and attended, a sequence forked, single tokens appended
+    to all and decoded, one freed, the pool compacted: the forked sequence
+    decodes like its parent, and compacting changes no bit of a decode."""
+    from sparse_long_context_03_b200 import inputs
+    cfg = inputs.config(3)
+    Hq, Hkv, D, HI, dI, k = cfg.Hq, cfg.Hkv, cfg.D, cfg.HI, cfg.dI, 256
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    c = dsa.KV8Cache(200, 6, 30, Hkv, D, dI=dI, scale_block=32)
+
+    def tokens(n):
+        kv = torch.randn(n, 2 * Hkv * D, generator=gen, device=DEV).to(torch.bfloat16)
+        k8, ks = inputs.quantize_e4m3_per_token(torch.randn(n, dI, generator=gen, device=DEV))
+        return kv[:, :Hkv * D].unflatten(1, (Hkv, D)), kv[:, Hkv * D:].unflatten(1, (Hkv, D)), k8, ks
+
+    # prompts in slots 0, 2 and 3, packed
+    slots, new = i32([0, 2, 3]), [700, 64, 333]
+    assert not c.extend(slots, i32(new)).any()
+    cu = i32(np.concatenate([[0], np.cumsum(new)]))
+    n = sum(new)
+    K, V, k8, ks = tokens(n)
+    c.append(K, V, cu, k8, ks, slots=slots)
+    plan = dsa.PrefillPlan(n, HI, dI, Hq, Hkv, D, k)
+    q8, sq = inputs.quantize_e4m3_per_token(torch.randn(n, HI, dI, generator=gen, device=DEV))
+    w = torch.rand(n, HI, generator=gen, device=DEV)
+    Q = torch.randn(n, Hq, D, generator=gen, device=DEV).to(torch.bfloat16)
+    O16, idx = torch.empty_like(Q), torch.empty(n, k, dtype=torch.int32, device=DEV)
+    dsa.prefill_forward_packed(plan, cu, q8, sq, w, k8, ks, Q, K.contiguous(), V.contiguous(), O16, idx_out=idx)
+    O8 = torch.empty_like(Q)
+    c.prefill(Q, idx, cu, O8, slots=slots)
+    # the cache holds K and V with a relative error of 2^-4 per value: the
+    # outputs agree as far as random errors of that size average out
+    a, b = O8.double(), O16.double()
+    assert ((a - b).norm() / b.norm()).item() < 0.06
+    # fork slot 0 to 4 and 5; one new token each, the same for all of them
+    assert not c.fork(i32([0, 0]), i32([4, 5])).any()
+    assert c.refcount.max().item() == 3
+    ws = torch.empty(dsa.decode_kv8_workspace_size(4, 1024, k), dtype=torch.uint8, device=DEV)
+    live = i32([0, 4, 5, 3])
+    for step in range(70):     # over a page's border
+        assert not c.extend(live, c.seq_lens[live.long()] + 1).any()
+        K, V, k8, ks = (t[:1].expand(4, *t.shape[1:]).contiguous() for t in tokens(1))
+        c.append(K, V, None, k8, ks, slots=live)
+    q = torch.randn(1, Hq, D, generator=gen, device=DEV).to(torch.bfloat16).expand(4, Hq, D).contiguous()
+    q8, sq = inputs.quantize_e4m3_per_token(torch.randn(1, HI, dI, generator=gen, device=DEV).expand(4, HI, dI))
+    w = torch.rand(1, HI, generator=gen, device=DEV).expand(4, HI).contiguous()
+    outs, sets = [], []
+    for _ in range(2):
+        out, sel = torch.empty(4, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(4, k, dtype=torch.int32, device=DEV)
+        c.decode(q, q8, sq, w, 1024, k, ws, out, idx_out=sel, slots=live)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+        assert torch.equal(sel[0], sel[1]) and not torch.equal(sel[0], sel[3])
+        outs.append(out)
+        sets.append(sel)
+        c.free(i32([2]))
+        page_map, used = c.compact()
+        assert int(used) == int((c.refcount > 0).sum()) and not c.refcount[int(used):].any()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(sets[0], sets[1])
+    c.free(i32([0, 3, 4, 5]))
+    assert not c.refcount.any() and bool((c.block_table == -1).all())
