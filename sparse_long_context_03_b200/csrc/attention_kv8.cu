@@ -234,7 +234,7 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, i
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMaxWarps * 32) sparse_kv8_kernel(const __grid_constant__ Kv8Args a) {
+__global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constant__ Kv8Args a) {
     extern __shared__ __align__(16) float part[];   // [W][8][D] sums, [W][8][2] (ref, l), the CTA's [8][2]
     const int lane = lane_id(), warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     cg::cluster_group cluster = cg::this_cluster();
@@ -266,7 +266,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sparse_kv8_kernel(const __grid
     Kv8State<D> st;
     init_state<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
 
-    // 32 keys a step, the pair's warps taking steps in turn
+    // 32 keys a step, the pair's warps taking steps in turn.  Nothing waits
+    // for what it has just asked for: the indices are read two steps ahead,
+    // the pages one, and a half step's K and V while the half before it is
+    // multiplied.
     const int step0 = crank * W + warp, nw = C * W, steps = (n_vis + 31) / 32;
     auto entry = [&](int step) {                    // the selected position, -1 if none
         const int e = step * 32 + lane;
@@ -274,19 +277,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sparse_kv8_kernel(const __grid
         return s <= t ? s : -1;
     };
     auto page_of = [&](int s) { return s >= 0 ? __ldg(bt + s / kPage) : -1; };
-    for (int step = step0; step < steps; step += nw) {
-        const int s = entry(step);
-        const int page = page_of(s);
-        int row = -1, meta = -1;
+    auto resolve = [&](int s, int page, int &row, int &meta) {
+        row = meta = -1;
         if (page >= 0 && page < a.num_pages) {
             row = page * kPage + s % kPage;
             meta = __ldg(a.exps + ((size_t)page * (kPage >> a.block_shift) + ((s % kPage) >> a.block_shift)) * a.Hkv + g);
         }
-        Tile<D> t0;
-        load_tile<D>(t0, row, 0, kg, vg, stride, lane);
-        attend_tile<D>(st, t0, meta, 0, lane);
-        load_tile<D>(t0, row, 1, kg, vg, stride, lane);
-        attend_tile<D>(st, t0, meta, 1, lane);
+    };
+    if (step0 < steps) {
+        Tile<D> ta, tb;
+        int row, meta;
+        int s0 = entry(step0), s1 = entry(step0 + nw);
+        int p0 = page_of(s0);
+        resolve(s0, p0, row, meta);
+        load_tile<D>(ta, row, 0, kg, vg, stride, lane);
+        s0 = s1;
+        p0 = page_of(s0);
+        s1 = entry(step0 + 2 * nw);
+        for (int step = step0; step < steps; step += nw) {
+            load_tile<D>(tb, row, 1, kg, vg, stride, lane);
+            const int meta_now = meta;
+            resolve(s0, p0, row, meta);             // the next step's rows; none behind the last
+            s0 = s1;
+            p0 = page_of(s0);
+            s1 = entry(step + 3 * nw);
+            attend_tile<D>(st, ta, meta_now, 0, lane);
+            load_tile<D>(ta, row, 0, kg, vg, stride, lane);
+            attend_tile<D>(st, tb, meta_now, 1, lane);
+        }
     }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
