@@ -425,8 +425,8 @@ DSA_API dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint1
 
 /* Decode stage 3 over the 8-bit cache: as dsa_sparse_gqa_decode_attention,
  * with the same treatment of index entries, pages and empty rows, and without
- * a workspace (a row's splits are joined on chip).  kv_exp is 2-byte aligned;
- * q, out and the caches are 16-byte aligned. */
+ * a workspace (a row's splits are joined on chip).  kv_exp is 2-byte aligned,
+ * q and out 16-byte, k_cache8 and v_cache8 32-byte. */
 DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_kv8(const uint16_t *q, const uint8_t *k_cache8,
                                                  const uint8_t *v_cache8, const uint8_t *kv_exp, int scale_block,
                                                  const int32_t *block_table, int max_pages, int num_pages,

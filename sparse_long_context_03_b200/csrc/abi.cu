@@ -416,7 +416,8 @@ static dsa_status_t check_kv8_attention(const void *q, const void *k_cache8, con
     if (rows == 0) return DSA_OK;
     if (!q || !k_cache8 || !v_cache8 || !kv_exp || !block_table || !seq_lens || !idx || !out)
         return DSA_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache8, 16) || !aligned(v_cache8, 16) ||
+    // a lane reads a quarter of a cached row at once
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache8, 32) || !aligned(v_cache8, 32) ||
         !aligned(kv_exp, 2))
         return DSA_ERR_INVALID_ARG;
     return DSA_OK;

@@ -22,13 +22,12 @@
 //
 // Work unit: one warp owns 16 keys of a (query, KV group) pair at a time, all
 // G <= 8 heads at once (keys on the matrix M dimension, heads on N = 8).  The
-// selected rows go from global memory straight to the registers of the lane
-// that multiplies them: for S = K Q^T any permutation of the head dims is
-// allowed as long as Q has the same, so a lane takes 16 consecutive bytes;
-// for O^T = V^T P^T a lane takes the same 16 dims of keys 2t, 2t+1, 2t+8 and
-// 2t+9 and pairs their bytes with a byte permute.  There is no shared-memory
-// stage, no swizzle and no transpose, and each lane ends with 16 consecutive
-// dims of two heads.
+// selected rows go from global memory straight to registers, a quarter of a
+// row to a lane.  For S = K Q^T any permutation of the head dims is allowed as
+// long as Q has the same, so the lane's bytes are operands as they are; for
+// O^T = V^T P^T a movmatrix per word takes them to the lanes that hold two
+// keys each, and a byte permute pairs the keys.  There is no shared-memory
+// stage and no swizzle.
 //
 // Pairs are split over several warps, and over the CTAs of a cluster, when
 // there are too few of them to fill the device; the partial results are
@@ -62,52 +61,57 @@ struct Kv8Args {
     float *lse;
 };
 
-// The K and V bytes of 16 keys, as each lane multiplies them.
+// The K and V bytes of 16 keys: each lane holds dims tig * D/4 .. + D/4 - 1 of
+// keys gid and gid + 8.
 template <int D>
 struct Tile {
-    uint32_t k[2][D / 64][4];    // keys gid, gid + 8: dims 64 j + 16 tig + 0..15
-    uint32_t v[4][D / 32];       // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: dims gid * D/8 + 0..
+    uint32_t k[2][D / 16], v[2][D / 16];
 };
 
+// A row's quarter in one load: 32 bytes (a 256-bit load) or 16.  The four
+// lanes of a key then read its whole row, which costs the fewest passes
+// through L1.
+__device__ __forceinline__ void ldg_stream(uint32_t (&r)[8], const uint8_t *p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
 __device__ __forceinline__ void ldg_stream(uint32_t (&r)[4], const uint8_t *p) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "l"(p));
 }
-__device__ __forceinline__ void ldg_stream(uint32_t (&r)[2], const uint8_t *p) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
-}
+
+// What stands for the rows of entries that select nothing: finite values whose
+// weight is zero.
+__device__ const uint4 g_zero_row[8] = {};
 
 // Issues the loads of keys half*16 .. +15 of the warp's 32: `row` holds, per
-// lane, the cache row of its key (-1: none, its bytes are taken as zero, so
-// that nothing of an unselected row reaches the products).
+// lane, the cache row of its key (-1: none); `all`: none is -1.  kg and vg
+// point at the lane's quarter of a row.
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, int row, int half, const uint8_t *kg, const uint8_t *vg,
-                                          uint32_t stride, int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
+__device__ __forceinline__ void load_tile(Tile<D> &t, int row, bool all, int half, const uint8_t *kg,
+                                          const uint8_t *vg, uint32_t stride, int lane) {
+    const int gid = lane >> 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + gid + 8 * i);
-        const uint8_t *p = kg + (uint64_t)(uint32_t)r * stride + tig * 16;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) t.k[i][j][w] = 0u;
-            if (r >= 0) ldg_stream(t.k[i][j], p + j * 64);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + 2 * tig + (i & 1) + 8 * (i >> 1));
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) t.v[i][w] = 0u;
-        if (r >= 0) ldg_stream(t.v[i], vg + (uint64_t)(uint32_t)r * stride + gid * (D / 8));
+        const uint64_t off = (uint64_t)(uint32_t)r * stride;
+        const uint8_t *pk = kg + off, *pv = vg + off;
+        if (!all && r < 0) pk = pv = reinterpret_cast<const uint8_t *>(g_zero_row) + (lane & 3) * (D / 4);
+        ldg_stream(t.k[i], pk);
+        ldg_stream(t.v[i], pv);
     }
 }
 
 // Running state of one warp: lane (gid, tig) holds heads 2 tig and 2 tig + 1;
-// o[m] are the products of one matrix instruction: dims gid * D/8 + 2 m
-// (o[m][0], o[m][1]) and + 2 m + 1 (o[m][2], o[m][3]) of the two heads.
+// o[w] are the products of one matrix instruction: dims d = dim_of(lane, w)
+// (o[w][0], o[w][1]) and d + 1 (o[w][2], o[w][3]) of the two heads.
+template <int D>
+__device__ __forceinline__ int dim_of(int gid, int w) {
+    return (gid >> 1) * (D / 4) + 4 * w + 2 * (gid & 1);
+}
+
 template <int D>
 struct Kv8State {
     uint32_t q[D / 16][2];
@@ -119,22 +123,20 @@ struct Kv8State {
 template <int D>
 __device__ __forceinline__ void init_state(Kv8State<D> &st, const uint16_t *qg, int G, float scale_log2, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
-    uint4 raw[D / 64][2];
+    constexpr int N = D / 32;                       // 16-byte pieces of the lane's quarter of a row
+    uint4 raw[N];
     uint32_t mx = 0;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j)
+    for (int j = 0; j < N; ++j) {
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (gid < G) raw[j] = __ldg(reinterpret_cast<const uint4 *>(qg + (size_t)gid * D + tig * (D / 4)) + j);
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            raw[j][h] = make_uint4(0, 0, 0, 0);
-            if (gid < G)
-                raw[j][h] = __ldg(reinterpret_cast<const uint4 *>(qg + (size_t)gid * D + j * 64 + tig * 16) + h);
-            const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mx = max(mx, (w[i] << 16) & 0x7FFF0000u);
-                mx = max(mx, w[i] & 0x7FFF0000u);
-            }
+        for (int i = 0; i < 4; ++i) {
+            mx = max(mx, (w[i] << 16) & 0x7FFF0000u);
+            mx = max(mx, w[i] & 0x7FFF0000u);
         }
+    }
     mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
     // largest |q| of the head's row is 2^(ef - 127) * 1.x; the factor is
@@ -142,19 +144,13 @@ __device__ __forceinline__ void init_state(Kv8State<D> &st, const uint16_t *qg, 
     const int ef = min(max((int)(mx >> 23), 15), 254);
     const float f = exp_byte_scale(268 - ef), inv = exp_byte_scale(ef - 14) * scale_log2;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j)
+    for (int j = 0; j < N; ++j) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
-            uint32_t p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                p[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
-            st.q[j * 4 + 2 * h][0] = p[0];
-            st.q[j * 4 + 2 * h][1] = p[1];
-            st.q[j * 4 + 2 * h + 1][0] = p[2];
-            st.q[j * 4 + 2 * h + 1][1] = p[3];
-        }
+        for (int i = 0; i < 4; ++i)
+            st.q[2 * j + i / 2][i & 1] =
+                pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+    }
     st.c[0] = __shfl_sync(0xFFFFFFFFu, inv, tig * 8);       // head 2 tig is row gid = 2 tig
     st.c[1] = __shfl_sync(0xFFFFFFFFu, inv, tig * 8 + 4);
 #pragma unroll
@@ -165,33 +161,38 @@ __device__ __forceinline__ void init_state(Kv8State<D> &st, const uint16_t *qg, 
     st.l[0] = st.l[1] = 0.f;
 }
 
-// `meta` holds, per lane, its key's exponent bytes (K low, V high) or -1.
+// What a key's scales come to, by the lane that looked the key up: `scales`
+// is K's scale as the upper half of a float and the inverse of V's as the
+// upper half in its lower half (powers of two: the halves are exact), `ev` is
+// V's exponent.  A key that does not exist has ev = -inf, so its weight is 0.
+struct KeyScales {
+    uint32_t scales;
+    float ev;
+};
+
 template <int D>
-__device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, int meta, int half, int lane) {
+__device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, const KeyScales &key, int half,
+                                            int lane) {
     const int gid = lane >> 2;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t x0 = t.k[0][j][w], x1 = t.k[1][j][w];
-            mma_f16_16816(s, e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
-                          e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)),
-                          st.q[j * 4 + w][0], st.q[j * 4 + w][1]);
-        }
-    const int m0 = __shfl_sync(0xFFFFFFFFu, meta, half * 16 + gid);
-    const int m8 = __shfl_sync(0xFFFFFFFFu, meta, half * 16 + gid + 8);
-    const float k0 = exp_byte_scale(m0 & 0xFF), k8 = exp_byte_scale(m8 & 0xFF);
-    const int e0 = (m0 >> 8) & 0xFF, e8 = (m8 >> 8) & 0xFF;
-    const float lv0 = m0 < 0 ? -INFINITY : (float)(e0 - 127), lv8 = m8 < 0 ? -INFINITY : (float)(e8 - 127);
-    const float iv0 = exp_byte_scale(254 - e0), iv8 = exp_byte_scale(254 - e8);
-    float u[4];
-    u[0] = m0 < 0 ? -INFINITY : fmaf(s[0], st.c[0] * k0, lv0);
-    u[1] = m0 < 0 ? -INFINITY : fmaf(s[1], st.c[1] * k0, lv0);
-    u[2] = m8 < 0 ? -INFINITY : fmaf(s[2], st.c[0] * k8, lv8);
-    u[3] = m8 < 0 ? -INFINITY : fmaf(s[3], st.c[1] * k8, lv8);
-    float mx[2] = {fmaxf(u[0], u[2]), fmaxf(u[1], u[3])};
-    if (__any_sync(0xFFFFFFFFu, mx[0] > st.ref[0] + 15.f || mx[1] > st.ref[1] + 15.f)) {
+    for (int w = 0; w < D / 16; ++w) {
+        const uint32_t x0 = t.k[0][w], x1 = t.k[1][w];
+        mma_f16_16816(s, e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
+                      e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)), st.q[w][0],
+                      st.q[w][1]);
+    }
+    const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, key.scales, half * 16 + gid);
+    const uint32_t s8 = __shfl_sync(0xFFFFFFFFu, key.scales, half * 16 + gid + 8);
+    const float ev0 = __shfl_sync(0xFFFFFFFFu, key.ev, half * 16 + gid);
+    const float ev8 = __shfl_sync(0xFFFFFFFFu, key.ev, half * 16 + gid + 8);
+    const float k0 = __uint_as_float(s0 & 0xFFFF0000u), k8 = __uint_as_float(s8 & 0xFFFF0000u);
+    const float iv0 = __uint_as_float(s0 << 16), iv8 = __uint_as_float(s8 << 16);
+    float u[4] = {fmaf(s[0], st.c[0] * k0, ev0), fmaf(s[1], st.c[1] * k0, ev0),
+                  fmaf(s[2], st.c[0] * k8, ev8), fmaf(s[3], st.c[1] * k8, ev8)};
+    float d[4] = {u[0] - st.ref[0], u[1] - st.ref[1], u[2] - st.ref[0], u[3] - st.ref[1]};
+    if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > 15.f)) {
+        float mx[2] = {fmaxf(u[0], u[2]), fmaxf(u[1], u[3])};
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
@@ -200,36 +201,34 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, i
         float alpha[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float ref = mx[i] > st.ref[i] + 15.f ? mx[i] - 7.f : st.ref[i];
+            const float ref = mx[i] - st.ref[i] > 15.f ? mx[i] - 7.f : st.ref[i];
             alpha[i] = fast_exp2(st.ref[i] - ref);
             st.ref[i] = ref;
             st.l[i] *= alpha[i];
+            d[i] = u[i] - ref;
+            d[2 + i] = u[2 + i] - ref;
         }
 #pragma unroll
-        for (int m = 0; m < D / 16; ++m) {
-            st.o[m][0] *= alpha[0];
-            st.o[m][1] *= alpha[1];
-            st.o[m][2] *= alpha[0];
-            st.o[m][3] *= alpha[1];
+        for (int w = 0; w < D / 16; ++w) {
+            st.o[w][0] *= alpha[0];
+            st.o[w][1] *= alpha[1];
+            st.o[w][2] *= alpha[0];
+            st.o[w][3] *= alpha[1];
         }
     }
-    const float p0 = fast_exp2(u[0] - st.ref[0]), p1 = fast_exp2(u[1] - st.ref[1]);
-    const float p2 = fast_exp2(u[2] - st.ref[0]), p3 = fast_exp2(u[3] - st.ref[1]);
-    // an unselected key has no weight: its scale byte (255) must not make 0 * inf
-    st.l[0] += (m0 < 0 ? 0.f : p0 * iv0) + (m8 < 0 ? 0.f : p2 * iv8);
-    st.l[1] += (m0 < 0 ? 0.f : p1 * iv0) + (m8 < 0 ? 0.f : p3 * iv8);
+    const float p0 = fast_exp2(d[0]), p1 = fast_exp2(d[1]), p2 = fast_exp2(d[2]), p3 = fast_exp2(d[3]);
+    st.l[0] = fmaf(p2, iv8, fmaf(p0, iv0, st.l[0]));
+    st.l[1] = fmaf(p3, iv8, fmaf(p1, iv0, st.l[1]));
     const uint32_t b0 = movmatrix_trans(pack_f16x2(p0, p1));
     const uint32_t b1 = movmatrix_trans(pack_f16x2(p2, p3));
+    // the transpose takes V from a lane per key to a lane per two keys, two
+    // dims at a time; the byte permute makes pairs of keys of one dim
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;   // two dims' bytes of two keys, by dim
-            const uint32_t x = __byte_perm(t.v[0][w], t.v[1][w], sel);
-            const uint32_t y = __byte_perm(t.v[2][w], t.v[3][w], sel);
-            mma_f16_16816(st.o[2 * w + h], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
-                          e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b0, b1);
-        }
+    for (int w = 0; w < D / 16; ++w) {
+        const uint32_t x = __byte_perm(movmatrix_trans(t.v[0][w]), 0u, 0x3120);
+        const uint32_t y = __byte_perm(movmatrix_trans(t.v[1][w]), 0u, 0x3120);
+        mma_f16_16816(st.o[w], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                      e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b0, b1);
     }
 }
 
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     const int n_vis = max(min(a.k, t + 1), 0);
     const int32_t *idx_row = a.idx + (size_t)r * a.k;
     const int32_t *bt = a.block_table + (size_t)b * a.max_pages;
-    const uint8_t *kg = a.kc + (size_t)g * D, *vg = a.vc + (size_t)g * D;
+    const uint8_t *kg = a.kc + (size_t)g * D + (lane & 3) * (D / 4), *vg = a.vc + (size_t)g * D + (lane & 3) * (D / 4);
     const uint32_t stride = (uint32_t)a.Hkv * D;
 
     Kv8State<D> st;
@@ -277,33 +276,39 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         return s <= t ? s : -1;
     };
     auto page_of = [&](int s) { return s >= 0 ? __ldg(bt + s / kPage) : -1; };
-    auto resolve = [&](int s, int page, int &row, int &meta) {
-        row = meta = -1;
+    int row;
+    bool all;
+    KeyScales key;
+    auto resolve = [&](int s, int page) {
+        row = -1;
+        key = {0x3F800000u, -INFINITY};
         if (page >= 0 && page < a.num_pages) {
             row = page * kPage + s % kPage;
-            meta = __ldg(a.exps + ((size_t)page * (kPage >> a.block_shift) + ((s % kPage) >> a.block_shift)) * a.Hkv + g);
+            const uint32_t e = __ldg(a.exps + ((size_t)page * (kPage >> a.block_shift) +
+                                               ((s % kPage) >> a.block_shift)) * a.Hkv + g);
+            key.scales = (e & 0xFFu) << 23 | (254u - (e >> 8)) << 7;
+            key.ev = (float)(int)(e >> 8) - 127.f;
         }
+        all = __all_sync(0xFFFFFFFFu, row >= 0);
     };
     if (step0 < steps) {
         Tile<D> ta, tb;
-        int row, meta;
         int s0 = entry(step0), s1 = entry(step0 + nw);
-        int p0 = page_of(s0);
-        resolve(s0, p0, row, meta);
-        load_tile<D>(ta, row, 0, kg, vg, stride, lane);
+        resolve(s0, page_of(s0));
+        load_tile<D>(ta, row, all, 0, kg, vg, stride, lane);
         s0 = s1;
-        p0 = page_of(s0);
+        int p0 = page_of(s0);
         s1 = entry(step0 + 2 * nw);
         for (int step = step0; step < steps; step += nw) {
-            load_tile<D>(tb, row, 1, kg, vg, stride, lane);
-            const int meta_now = meta;
-            resolve(s0, p0, row, meta);             // the next step's rows; none behind the last
+            load_tile<D>(tb, row, all, 1, kg, vg, stride, lane);
+            const KeyScales now = key;
+            resolve(s0, p0);                        // the next step's rows; none behind the last
             s0 = s1;
             p0 = page_of(s0);
             s1 = entry(step + 3 * nw);
-            attend_tile<D>(st, ta, meta_now, 0, lane);
-            load_tile<D>(ta, row, 0, kg, vg, stride, lane);
-            attend_tile<D>(st, tb, meta_now, 1, lane);
+            attend_tile<D>(st, ta, now, 0, lane);
+            load_tile<D>(ta, row, all, 0, kg, vg, stride, lane);
+            attend_tile<D>(st, tb, now, 1, lane);
         }
     }
 #pragma unroll
@@ -320,12 +325,10 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
             const int h = 2 * tig + i;
             if (h >= G) continue;
             const float inv = st.l[i] > 0.f ? 1.f / st.l[i] : 0.f;
-            uint32_t w[D / 16];
 #pragma unroll
-            for (int m = 0; m < D / 16; ++m) w[m] = pack_bf16x2(st.o[m][i] * inv, st.o[m][2 + i] * inv);
-            uint4 *dst = reinterpret_cast<uint4 *>(og + (size_t)h * D + gid * (D / 8));
-#pragma unroll
-            for (int m = 0; m < D / 64; ++m) dst[m] = make_uint4(w[4 * m], w[4 * m + 1], w[4 * m + 2], w[4 * m + 3]);
+            for (int w = 0; w < D / 16; ++w)
+                *reinterpret_cast<uint32_t *>(og + (size_t)h * D + dim_of<D>(gid, w)) =
+                    pack_bf16x2(st.o[w][i] * inv, st.o[w][2 + i] * inv);
             if (lg != nullptr && gid == 0) lg[h] = st.l[i] > 0.f ? (st.ref[i] + __log2f(st.l[i])) * kLn2 : -INFINITY;
         }
         return;
@@ -334,10 +337,10 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     float *ml = part + (size_t)W * 8 * D, *cta_ml = ml + W * 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)warp * 8 + 2 * tig + i) * D + gid * (D / 8));
 #pragma unroll
-        for (int m = 0; m < D / 32; ++m)
-            dst[m] = make_float4(st.o[2 * m][i], st.o[2 * m][2 + i], st.o[2 * m + 1][i], st.o[2 * m + 1][2 + i]);
+        for (int w = 0; w < D / 16; ++w)
+            *reinterpret_cast<float2 *>(part + ((size_t)warp * 8 + 2 * tig + i) * D + dim_of<D>(gid, w)) =
+                make_float2(st.o[w][i], st.o[w][2 + i]);
         if (gid == 0) {
             ml[(warp * 8 + 2 * tig + i) * 2] = st.ref[i];
             ml[(warp * 8 + 2 * tig + i) * 2 + 1] = st.l[i];
@@ -434,8 +437,10 @@ cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
     cfg.blockDim = dim3(sp.warps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    // only where it is needed: an SM holds 8 CTAs of a cluster launch, even of
+    // clusters of one, but 12 one-warp CTAs of a plain one
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = sp.ctas > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, sparse_kv8_kernel<D>, a);
 }
 

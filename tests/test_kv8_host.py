@@ -58,7 +58,7 @@ def test_append_refusals(lib, kw, want):
     (dict(n=-1), INVALID), (dict(k=0), INVALID), (dict(Hq=30), UNSUPPORTED), (dict(Hq=36), UNSUPPORTED),
     (dict(D=96), UNSUPPORTED), (dict(block=128), UNSUPPORTED), (dict(num_pages=1 << 25), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(idx=None), INVALID), (dict(out=None), INVALID), (dict(out=B + 8), INVALID),
-    (dict(q=B + 2), INVALID), (dict(exp=B + 1), INVALID), (dict(kc=B + 4), INVALID), (dict(max_pages=0), INVALID),
+    (dict(q=B + 2), INVALID), (dict(exp=B + 1), INVALID), (dict(kc=B + 16), INVALID), (dict(vc=B + 16), INVALID), (dict(max_pages=0), INVALID),
     (dict(n=2 ** 29), UNSUPPORTED), (dict(n=0), OK),
 ])
 @pytest.mark.parametrize("prefill", [False, True])
