@@ -86,21 +86,18 @@ __device__ __forceinline__ void ldg_stream(uint32_t (&r)[4], const uint8_t *p) {
 // weight is zero.
 __device__ const uint4 g_zero_row[8] = {};
 
-// Issues the loads of keys half*16 .. +15 of the warp's 32: `row` holds, per
-// lane, the cache row of its key (-1: none); `all`: none is -1.  kg and vg
-// point at the lane's quarter of a row.
+// Issues the loads of K or V (`to`, from `base`) of keys half*16 .. +15 of the
+// warp's 32: `row` holds, per lane, the cache row of its key (-1: none);
+// `all`: none is -1.  base points at the lane's quarter of a row.
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, int row, bool all, int half, const uint8_t *kg,
-                                          const uint8_t *vg, uint32_t stride, int lane) {
-    const int gid = lane >> 2;
+__device__ __forceinline__ void load_half(uint32_t (&to)[2][D / 16], int row, bool all, int half, const uint8_t *base,
+                                          uint32_t stride, int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + gid + 8 * i);
-        const uint64_t off = (uint64_t)(uint32_t)r * stride;
-        const uint8_t *pk = kg + off, *pv = vg + off;
-        if (!all && r < 0) pk = pv = reinterpret_cast<const uint8_t *>(g_zero_row) + (lane & 3) * (D / 4);
-        ldg_stream(t.k[i], pk);
-        ldg_stream(t.v[i], pv);
+        const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + (lane >> 2) + 8 * i);
+        const uint8_t *p = base + (uint64_t)(uint32_t)r * stride;
+        if (!all && r < 0) p = reinterpret_cast<const uint8_t *>(g_zero_row) + (lane & 3) * (D / 4);
+        ldg_stream(to[i], p);
     }
 }
 
@@ -170,9 +167,11 @@ struct KeyScales {
     float ev;
 };
 
-template <int D>
-__device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, const KeyScales &key, int half,
-                                            int lane) {
+// Multiplies tile t; next_k and next_v issue the loads that take its place, as
+// soon as its registers are read.
+template <int D, typename NextK, typename NextV>
+__device__ __forceinline__ void attend_tile(Kv8State<D> &st, Tile<D> &t, const KeyScales &key, int half, int lane,
+                                            NextK next_k, NextV next_v) {
     const int gid = lane >> 2;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -182,6 +181,7 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, c
                       e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)), st.q[w][0],
                       st.q[w][1]);
     }
+    next_k();
     const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, key.scales, half * 16 + gid);
     const uint32_t s8 = __shfl_sync(0xFFFFFFFFu, key.scales, half * 16 + gid + 8);
     const float ev0 = __shfl_sync(0xFFFFFFFFu, key.ev, half * 16 + gid);
@@ -230,6 +230,7 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, const Tile<D> &t, c
         mma_f16_16816(st.o[w], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
                       e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b0, b1);
     }
+    next_v();
 }
 
 template <int D>
@@ -266,9 +267,9 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     init_state<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
 
     // 32 keys a step, the pair's warps taking steps in turn.  Nothing waits
-    // for what it has just asked for: the indices are read two steps ahead,
-    // the pages one, and a half step's K and V while the half before it is
-    // multiplied.
+    // for what it has just asked for: the indices are read three steps ahead,
+    // the pages two, and the next step's K and V are asked for as soon as the
+    // registers that this step's took are free.
     const int step0 = crank * W + warp, nw = C * W, steps = (n_vis + 31) / 32;
     auto entry = [&](int step) {                    // the selected position, -1 if none
         const int e = step * 32 + lane;
@@ -292,23 +293,28 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         all = __all_sync(0xFFFFFFFFu, row >= 0);
     };
     if (step0 < steps) {
-        Tile<D> ta, tb;
+        Tile<D> tile[2];
         int s0 = entry(step0), s1 = entry(step0 + nw);
         resolve(s0, page_of(s0));
-        load_tile<D>(ta, row, all, 0, kg, vg, stride, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            load_half<D>(tile[h].k, row, all, h, kg, stride, lane);
+            load_half<D>(tile[h].v, row, all, h, vg, stride, lane);
+        }
         s0 = s1;
         int p0 = page_of(s0);
         s1 = entry(step0 + 2 * nw);
         for (int step = step0; step < steps; step += nw) {
-            load_tile<D>(tb, row, all, 1, kg, vg, stride, lane);
             const KeyScales now = key;
             resolve(s0, p0);                        // the next step's rows; none behind the last
             s0 = s1;
             p0 = page_of(s0);
             s1 = entry(step + 3 * nw);
-            attend_tile<D>(st, ta, now, 0, lane);
-            load_tile<D>(ta, row, all, 0, kg, vg, stride, lane);
-            attend_tile<D>(st, tb, now, 1, lane);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                attend_tile<D>(
+                    st, tile[h], now, h, lane, [&] { load_half<D>(tile[h].k, row, all, h, kg, stride, lane); },
+                    [&] { load_half<D>(tile[h].v, row, all, h, vg, stride, lane); });
         }
     }
 #pragma unroll
