@@ -118,7 +118,17 @@ struct Kv8State {
 };
 
 template <int D>
-__device__ __forceinline__ void init_state(Kv8State<D> &st, const uint16_t *qg, int G, float scale_log2, int lane) {
+__device__ __forceinline__ void clear_sums(Kv8State<D> &st) {
+#pragma unroll
+    for (int w = 0; w < D / 16; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[w][i] = 0.f;
+    st.ref[0] = st.ref[1] = kRefNone;
+    st.l[0] = st.l[1] = 0.f;
+}
+
+template <int D>
+__device__ __forceinline__ void load_q(Kv8State<D> &st, const uint16_t *qg, int G, float scale_log2, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
     constexpr int N = D / 32;                       // 16-byte pieces of the lane's quarter of a row
     uint4 raw[N];
@@ -150,12 +160,6 @@ __device__ __forceinline__ void init_state(Kv8State<D> &st, const uint16_t *qg, 
     }
     st.c[0] = __shfl_sync(0xFFFFFFFFu, inv, tig * 8);       // head 2 tig is row gid = 2 tig
     st.c[1] = __shfl_sync(0xFFFFFFFFu, inv, tig * 8 + 4);
-#pragma unroll
-    for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[m][i] = 0.f;
-    st.ref[0] = st.ref[1] = kRefNone;
-    st.l[0] = st.l[1] = 0.f;
 }
 
 // What a key's scales come to, by the lane that looked the key up: `scales`
@@ -244,6 +248,19 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     const int g = a.group_major ? pair / a.n_rows : pair % a.Hkv;
     const int G = a.Hq / a.Hkv;
 
+    // 32 keys a step, the pair's warps taking steps in turn.  Nothing waits
+    // for what it has just asked for: the indices are read three steps ahead,
+    // the pages two, and the next step's K and V are asked for as soon as the
+    // registers that this step's took are free.  The first indices are asked
+    // for before the sequence's length is known.
+    const int32_t *idx_row = a.idx + (size_t)r * a.k;
+    const int step0 = crank * W + warp, nw = C * W;
+    auto index_at = [&](int step) {
+        const int e = step * 32 + lane;
+        return e < a.k ? __ldg(idx_row + e) : -1;
+    };
+    const int first = index_at(step0), second = index_at(step0 + nw);
+
     // the query's sequence b and position t; rows outside every sequence are
     // left as they are (the same answer in every CTA of a cluster)
     int b, t;
@@ -258,24 +275,12 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     }
     t = min(t, a.max_pages * kPage - 1);
     const int n_vis = max(min(a.k, t + 1), 0);
-    const int32_t *idx_row = a.idx + (size_t)r * a.k;
     const int32_t *bt = a.block_table + (size_t)b * a.max_pages;
     const uint8_t *kg = a.kc + (size_t)g * D + (lane & 3) * (D / 4), *vg = a.vc + (size_t)g * D + (lane & 3) * (D / 4);
     const uint32_t stride = (uint32_t)a.Hkv * D;
-
-    Kv8State<D> st;
-    init_state<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
-
-    // 32 keys a step, the pair's warps taking steps in turn.  Nothing waits
-    // for what it has just asked for: the indices are read three steps ahead,
-    // the pages two, and the next step's K and V are asked for as soon as the
-    // registers that this step's took are free.
-    const int step0 = crank * W + warp, nw = C * W, steps = (n_vis + 31) / 32;
-    auto entry = [&](int step) {                    // the selected position, -1 if none
-        const int e = step * 32 + lane;
-        const int s = e < n_vis ? __ldg(idx_row + e) : -1;
-        return s <= t ? s : -1;
-    };
+    const int steps = (n_vis + 31) / 32;
+    // of an index read, the selected position; -1 if it is none
+    auto position = [&](int s, int step) { return step * 32 + lane < n_vis && s <= t ? s : -1; };
     auto page_of = [&](int s) { return s >= 0 ? __ldg(bt + s / kPage) : -1; };
     int row;
     bool all;
@@ -292,9 +297,11 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         }
         all = __all_sync(0xFFFFFFFFu, row >= 0);
     };
+    Kv8State<D> st;
+    clear_sums<D>(st);
     if (step0 < steps) {
         Tile<D> tile[2];
-        int s0 = entry(step0), s1 = entry(step0 + nw);
+        int s0 = position(first, step0), s1 = position(second, step0 + nw);
         resolve(s0, page_of(s0));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -303,17 +310,22 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         }
         s0 = s1;
         int p0 = page_of(s0);
-        s1 = entry(step0 + 2 * nw);
+        s1 = index_at(step0 + 2 * nw);
+        load_q<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
         for (int step = step0; step < steps; step += nw) {
             const KeyScales now = key;
-            resolve(s0, p0);                        // the next step's rows; none behind the last
-            s0 = s1;
+            // the next step's rows; none behind the last step, whose loads then
+            // read zeros from L1 (a branch around them would make them wait:
+            // 436 us became 752 on a 2048-row prompt chunk)
+            resolve(s0, p0);
+            s0 = position(s1, step + 2 * nw);
             p0 = page_of(s0);
-            s1 = entry(step + 3 * nw);
+            s1 = index_at(step + 3 * nw);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 attend_tile<D>(
-                    st, tile[h], now, h, lane, [&] { load_half<D>(tile[h].k, row, all, h, kg, stride, lane); },
+                    st, tile[h], now, h, lane,
+                    [&] { load_half<D>(tile[h].k, row, all, h, kg, stride, lane); },
                     [&] { load_half<D>(tile[h].v, row, all, h, vg, stride, lane); });
         }
     }
