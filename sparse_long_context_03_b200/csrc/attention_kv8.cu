@@ -14,20 +14,23 @@
 // of a maximum over the warp.
 //
 // e4m3 converts to fp16 without loss, and the products run on fp16 matrix
-// instructions with fp32 sums.  Q is bf16: each head's row is multiplied by
-// the power of two that puts its largest value into [2^14, 2^15), after which
-// fp16 holds every bf16 value that is not 2^-30 of the largest exactly; the
-// weights are rounded to fp16 (2^-11, half of what bf16 would cost twice
-// over), the sums are of the unrounded weights.
+// instructions with fp32 sums.  (The warp-level 8-bit matrix instructions are
+// no way around the conversions: on this chip they are carried out as
+// conversions and fp16 products, and with Q and the weights as sums of 8-bit
+// parts a 2048-row prompt chunk took 786 us.)  Q is bf16: each head's row is
+// multiplied by the power of two that puts its largest value into [2^14,
+// 2^15), after which fp16 holds every bf16 value that is 2^-30 of the largest
+// or more exactly; the weights are rounded to fp16 (2^-11, an eighth of what
+// bf16 would lose), the sums are of the unrounded weights.
 //
 // Work unit: one warp owns 16 keys of a (query, KV group) pair at a time, all
 // G <= 8 heads at once (keys on the matrix M dimension, heads on N = 8).  The
 // selected rows go from global memory straight to registers, a quarter of a
 // row to a lane.  For S = K Q^T any permutation of the head dims is allowed as
 // long as Q has the same, so the lane's bytes are operands as they are; for
-// O^T = V^T P^T a movmatrix per word takes them to the lanes that hold two
-// keys each, and a byte permute pairs the keys.  There is no shared-memory
-// stage and no swizzle.
+// O^T = V^T P^T the converted pairs of dims pass through a movmatrix each, to
+// the lanes that hold two keys of a dim.  There is no shared-memory stage and
+// no swizzle.
 //
 // Pairs are split over several warps, and over the CTAs of a cluster, when
 // there are too few of them to fill the device; the partial results are
@@ -102,8 +105,10 @@ __device__ __forceinline__ void load_half(uint32_t (&to)[2][D / 16], int row, bo
 }
 
 // Running state of one warp: lane (gid, tig) holds heads 2 tig and 2 tig + 1;
-// o[w] are the products of one matrix instruction: dims d = dim_of(lane, w)
-// (o[w][0], o[w][1]) and d + 1 (o[w][2], o[w][3]) of the two heads.
+// o[w] are the products of one matrix instruction, for dims d = (gid / 2) *
+// D/4 + 4 w + gid % 2 (o[w][0], o[w][1]) and d + 2 (o[w][2], o[w][3]) of the
+// two heads; at the end lanes of even and odd gid exchange one of the two, so
+// that each has dims dim_of(gid, w) and the next.
 template <int D>
 __device__ __forceinline__ int dim_of(int gid, int w) {
     return (gid >> 1) * (D / 4) + 4 * w + 2 * (gid & 1);
@@ -225,21 +230,41 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, Tile<D> &t, const K
     st.l[1] = fmaf(p3, iv8, fmaf(p1, iv0, st.l[1]));
     const uint32_t b0 = movmatrix_trans(pack_f16x2(p0, p1));
     const uint32_t b1 = movmatrix_trans(pack_f16x2(p2, p3));
-    // the transpose takes V from a lane per key to a lane per two keys, two
-    // dims at a time; the byte permute makes pairs of keys of one dim
+    // a movmatrix takes a pair of dims from a lane per key to a lane per two
+    // keys
 #pragma unroll
     for (int w = 0; w < D / 16; ++w) {
-        const uint32_t x = __byte_perm(movmatrix_trans(t.v[0][w]), 0u, 0x3120);
-        const uint32_t y = __byte_perm(movmatrix_trans(t.v[1][w]), 0u, 0x3120);
-        mma_f16_16816(st.o[w], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
-                      e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b0, b1);
+        const uint32_t x = t.v[0][w], y = t.v[1][w];
+        mma_f16_16816(st.o[w], movmatrix_trans(e4m3x2_to_f16x2((uint16_t)x)),
+                      movmatrix_trans(e4m3x2_to_f16x2((uint16_t)(x >> 16))),
+                      movmatrix_trans(e4m3x2_to_f16x2((uint16_t)y)),
+                      movmatrix_trans(e4m3x2_to_f16x2((uint16_t)(y >> 16))), b0, b1);
     }
     next_v();
 }
 
+// Shared memory of a joined pair: a part per warp (its sums), then what the
+// joining of the warps and of the cluster's CTAs takes.  The sums' heads and quarters
+// of a row lie so far apart that the lanes' stores meet no bank twice.
+template <int D>
+struct Join {
+    static constexpr int kQuarter = D == 128 ? 36 : 16, kHead = D == 128 ? 148 : 66, kWarp = 8 * kHead;
+    static __device__ __forceinline__ int at(int head, int dim) {
+        return head * kHead + dim / (D / 4) * kQuarter + dim % (D / 4);
+    }
+    static size_t bytes(int warps, int ctas, int G) {
+        const size_t slice = ((size_t)G * (D / 2) + ctas - 1) / ctas;
+        if (warps * ctas == 1) return 0;
+        size_t n = (size_t)warps * (kWarp * sizeof(float) + 8 * (sizeof(float2) + sizeof(float)));
+        if (ctas > 1) n += ctas * (8 + slice) * sizeof(float2);
+        return n;
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constant__ Kv8Args a) {
-    extern __shared__ __align__(16) float part[];   // [W][8][D] sums, [W][8][2] (ref, l), the CTA's [8][2]
+    extern __shared__ __align__(16) float smem[];
+    using S = Join<D>;
     const int lane = lane_id(), warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
@@ -297,6 +322,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         }
         all = __all_sync(0xFFFFFFFFu, row >= 0);
     };
+    if (C > 1) cluster_arrive();                    // waited for before the first store to another CTA
     Kv8State<D> st;
     clear_sums<D>(st);
     if (step0 < steps) {
@@ -335,6 +361,15 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         st.l[1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[1], o);
     }
     const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int w = 0; w < D / 16; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = st.o[w][i], y = st.o[w][2 + i];
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, gid & 1 ? x : y, 4);
+            st.o[w][i] = gid & 1 ? other : x;
+            st.o[w][2 + i] = gid & 1 ? y : other;
+        }
     uint16_t *og = a.out + ((size_t)r * a.Hq + (size_t)g * G) * D;
     float *lg = a.lse != nullptr ? a.lse + (size_t)r * a.Hq + (size_t)g * G : nullptr;
     if (nw == 1) {
@@ -352,76 +387,78 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         return;
     }
     // join the warps' sums: within the CTA, then across the cluster
-    float *ml = part + (size_t)W * 8 * D, *cta_ml = ml + W * 16;
+    float2 *ml = reinterpret_cast<float2 *>(smem + W * S::kWarp);   // [W][8] (ref, l)
+    float *factor = reinterpret_cast<float *>(ml + W * 8);          // [W][8]
+    float2 *recv_ml = reinterpret_cast<float2 *>(factor + W * 8);   // [C][8], from the cluster's CTAs
+    float2 *recv = recv_ml + C * 8;                                 // [C][slice]
+    float *own = smem + warp * S::kWarp;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int w = 0; w < D / 16; ++w)
-            *reinterpret_cast<float2 *>(part + ((size_t)warp * 8 + 2 * tig + i) * D + dim_of<D>(gid, w)) =
+            *reinterpret_cast<float2 *>(own + S::at(2 * tig + i, dim_of<D>(gid, w))) =
                 make_float2(st.o[w][i], st.o[w][2 + i]);
-        if (gid == 0) {
-            ml[(warp * 8 + 2 * tig + i) * 2] = st.ref[i];
-            ml[(warp * 8 + 2 * tig + i) * 2 + 1] = st.l[i];
+        if (gid == 0) ml[warp * 8 + 2 * tig + i] = make_float2(st.ref[i], st.l[i]);
+    }
+    __syncthreads();
+    float M = kRefNone, L = 0.f;                                    // of head threadIdx.x, if below G
+    if ((int)threadIdx.x < G) {
+        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * 8 + threadIdx.x].x);
+        for (int w = 0; w < W; ++w) {
+            const float2 x = ml[w * 8 + threadIdx.x];
+            const float f = fast_exp2(x.x - M);
+            factor[w * 8 + threadIdx.x] = f;
+            L = fmaf(x.y, f, L);
+        }
+        if (C == 1) {
+            if (lg != nullptr) lg[threadIdx.x] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+            ml[threadIdx.x] = make_float2(L > 0.f ? 1.f / L : 0.f, 0.f);
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < G * (D / 2); e += blockDim.x) {
+    const int n = G * (D / 2), slice = (n + C - 1) / C;
+    if (C > 1) {
+        cluster_wait();
+        if ((int)threadIdx.x < G)
+            for (int c = 0; c < C; ++c)
+                cluster.map_shared_rank(recv_ml, c)[crank * 8 + threadIdx.x] = make_float2(M, L);
+    }
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
         const int h = e / (D / 2), d = e % (D / 2) * 2;
-        float M = kRefNone;
-        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[(w * 8 + h) * 2]);
-        float L = 0.f, x = 0.f, y = 0.f;
+        float x = 0.f, y = 0.f;
+#pragma unroll 4
         for (int w = 0; w < W; ++w) {
-            const float f = fast_exp2(ml[(w * 8 + h) * 2] - M);
-            const float2 v = *reinterpret_cast<const float2 *>(part + ((size_t)w * 8 + h) * D + d);
-            L = fmaf(ml[(w * 8 + h) * 2 + 1], f, L);
+            const float f = factor[w * 8 + h];
+            const float2 v = *reinterpret_cast<const float2 *>(smem + w * S::kWarp + S::at(h, d));
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
         }
         if (C == 1) {
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = ml[h].x;
             *reinterpret_cast<uint32_t *>(og + (size_t)h * D + d) = pack_bf16x2(x * inv, y * inv);
-            if (lg != nullptr && d == 0) lg[h] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
         } else {
-            *reinterpret_cast<float2 *>(part + (size_t)h * D + d) = make_float2(x, y);  // this thread's own place
-            if (d == 0) {
-                cta_ml[h * 2] = M;
-                cta_ml[h * 2 + 1] = L;
-            }
+            cluster.map_shared_rank(recv, e / slice)[crank * slice + e % slice] = make_float2(x, y);
         }
     }
     if (C == 1) return;
     cluster.sync();
-    for (int e = crank * (int)blockDim.x + threadIdx.x; e < G * (D / 2); e += C * blockDim.x) {
+    for (int i = threadIdx.x; i < slice; i += blockDim.x) {
+        const int e = crank * slice + i;
+        if (e >= n) break;
         const int h = e / (D / 2), d = e % (D / 2) * 2;
-        float ref[kMaxCluster], l[kMaxCluster];
-        float2 v[kMaxCluster];
-        float M = kRefNone;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            ref[c] = kRefNone;
-            l[c] = 0.f;
-            v[c] = make_float2(0.f, 0.f);
-            if (c < C) {
-                const float2 m = *reinterpret_cast<const float2 *>(cluster.map_shared_rank(cta_ml, c) + h * 2);
-                ref[c] = m.x;
-                l[c] = m.y;
-                v[c] = *reinterpret_cast<const float2 *>(cluster.map_shared_rank(part, c) + (size_t)h * D + d);
-            }
-            M = fmaxf(M, ref[c]);
+        float top = kRefNone, sum = 0.f, x = 0.f, y = 0.f;
+        for (int c = 0; c < C; ++c) top = fmaxf(top, recv_ml[c * 8 + h].x);
+        for (int c = 0; c < C; ++c) {
+            const float2 m = recv_ml[c * 8 + h], v = recv[c * slice + i];
+            const float f = fast_exp2(m.x - top);
+            sum = fmaf(m.y, f, sum);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
         }
-        float L = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            const float f = fast_exp2(ref[c] - M);
-            L = fmaf(l[c], f, L);
-            x = fmaf(v[c].x, f, x);
-            y = fmaf(v[c].y, f, y);
-        }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
         *reinterpret_cast<uint32_t *>(og + (size_t)h * D + d) = pack_bf16x2(x * inv, y * inv);
-        if (lg != nullptr && d == 0) lg[h] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        if (lg != nullptr && d == 0) lg[h] = sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
     }
-    cluster.sync();  // the cluster's shared memory is read until here
 }
 
 // How many warps share a pair, and in how many CTAs: enough that the pairs'
@@ -445,7 +482,9 @@ cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
     constexpr int kSlots = 148 * 12;  // SMs x warps that the registers of a lane allow
     const int64_t pairs = (int64_t)a.n_rows * a.Hkv;
     const Split sp = split_of(pairs, a.k, kSlots);
-    const size_t smem = sp.warps * sp.ctas > 1 ? ((size_t)sp.warps * (8 * D + 16) + 16) * sizeof(float) : 0;
+    const size_t smem = Join<D>::bytes(sp.warps, sp.ctas, a.Hq / a.Hkv);
+    static_assert(kMaxWarps * (Join<D>::kWarp + 24) * sizeof(float) + 8 * (D / 2 + 8 + kMaxCluster) * sizeof(float2) <= 48 << 10,
+                  "within the default limit of dynamic shared memory");
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)sp.ctas;

@@ -63,6 +63,11 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Another CTA's shared memory may be written once that CTA has started: every
+// thread arrives early and waits before its first store to it.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
+
 // The largest b in [0, nseq) with first(b) <= key, by one warp: each round
 // probes 32 places, so that up to 32 sequences take one load latency and
 // 1024 two.  first must not decrease; first(0) <= key is taken for granted.

@@ -15,6 +15,7 @@
 #include <cooperative_groups.h>
 
 #include "kernels.h"
+#include "kv8.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -43,11 +44,6 @@ __device__ __forceinline__ Stretch stretch_of(int num_pages, int warps, int w) {
     const long long b = (long long)per * w;
     return {(int)min(b, (long long)num_pages), (int)min(b + per, (long long)num_pages)};
 }
-
-// Another CTA's shared memory may be written once that CTA has started: every
-// thread arrives at the kernel's start and waits before the first exchange.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
 
 // Sum over the cluster's warps before this one, and over all of them, of a
 // warp's count.  Ends with a cluster-wide barrier before the sums are read.
