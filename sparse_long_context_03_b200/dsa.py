@@ -498,68 +498,80 @@ KV8_EXP_MIN = 87  # the least scale exponent byte: 2^-40
 
 
 def _shaped(t, dtype, shape, name, device):
-    """``t`` is a dense tensor of this type and shape on ``device``."""
-    if t.dtype != dtype:
+    """``t`` is a dense tensor of this type and shape on CUDA device ``device``."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _device_of(t, name):
-    if not t.is_cuda:
+    """The index of a tensor's CUDA device."""
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    return t.device
+    return device
 
 
 def _call(name, device, stream, *args):
     """The entry point, on ``device`` (made current if it is not) and on the
     given stream or that device's current one."""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), name)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)  # a tenth of what current_stream() costs
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
+    if device == torch.cuda.current_device():
+        code = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)), name)
+            code = fn(*args, stream)
+    if code:
+        _check(code, name)
 
 
 def _kv8_cache(k_cache8, v_cache8, kv_exp):
-    """Checks the three buffers of an 8-bit cache; (num_pages, Hkv, D, scale_block)."""
+    """Checks the three buffers of an 8-bit cache; (device, num_pages, Hkv, D, scale_block)."""
     device = _device_of(k_cache8, "k_cache8")
-    if k_cache8.dim() != 4 or k_cache8.shape[1] != PAGE_SIZE:
-        raise ValueError(f"k_cache8: expected [num_pages, {PAGE_SIZE}, Hkv, D], got {tuple(k_cache8.shape)}")
-    P, _, Hkv, D = k_cache8.shape
-    _shaped(k_cache8, torch.uint8, (P, PAGE_SIZE, Hkv, D), "k_cache8", device)
-    _shaped(v_cache8, torch.uint8, (P, PAGE_SIZE, Hkv, D), "v_cache8", device)
+    shape = k_cache8.shape
+    if len(shape) != 4 or shape[1] != PAGE_SIZE:
+        raise ValueError(f"k_cache8: expected [num_pages, {PAGE_SIZE}, Hkv, D], got {tuple(shape)}")
+    P, _, Hkv, D = shape
+    _shaped(k_cache8, torch.uint8, shape, "k_cache8", device)
+    _shaped(v_cache8, torch.uint8, shape, "v_cache8", device)
     parts = kv_exp.shape[1] if kv_exp.dim() == 4 else 0
     if parts not in (1, 2, 4):
         raise ValueError(f"kv_exp: expected [num_pages, 1, 2 or 4, Hkv, 2], got {tuple(kv_exp.shape)}")
     _shaped(kv_exp, torch.uint8, (P, parts, Hkv, 2), "kv_exp", device)
-    return P, Hkv, D, PAGE_SIZE // parts
+    return device, P, Hkv, D, PAGE_SIZE // parts
 
 
 def _token_rows(t, n, Hkv, D, name, device):
     """Checks [n, Hkv, D] bf16 rows that may lie apart; the distance in elements."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (n, Hkv, D):
+    if t.shape != (n, Hkv, D):
         raise ValueError(f"{name}: expected shape {(n, Hkv, D)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected on {device}, got {t.device}")
-    if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D):
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected on cuda:{device}, got {t.device}")
+    ld, head, one = t.stride()
+    if one != 1 or (Hkv > 1 and head != D):
         raise ValueError(f"{name}: a token's [Hkv, D] values must be contiguous")
-    return t.stride(0) if n > 1 else Hkv * D
+    return ld if n > 1 else Hkv * D
 
 
 def _table(block_table, seq_lens, n, device):
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table: expected 2 dims, got shape {tuple(block_table.shape)}")
-    _shaped(block_table, torch.int32, (n, block_table.shape[1]), "block_table", device)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError(f"block_table: expected [{n}, max_pages], got shape {tuple(shape)}")
+    _shaped(block_table, torch.int32, shape, "block_table", device)
     _shaped(seq_lens, torch.int32, (n,), "seq_lens", device)
-    return block_table.shape[1]
+    return shape[1]
 
 
 def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqlens=None, k8=None, k_scale=None,
@@ -569,8 +581,7 @@ def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqle
     seq_lens [nseq] count them already.  cu_seqlens int32 [nseq+1] for packed
     new tokens, None for one per sequence.  k8 [n, dI] uint8 and k_scale [n]
     float32, with their caches, add the indexer's keys."""
-    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
-    device = k_cache8.device
+    device, P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
     n, nseq = K.shape[0], seq_lens.shape[0]
     ld_k = _token_rows(K, n, Hkv, D, "K", device)
     ld_v = _token_rows(V, n, Hkv, D, "V", device)
@@ -590,20 +601,21 @@ def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqle
         _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
     elif k_scale is not None or k8_cache is not None or k_scale_cache is not None:
         raise ValueError("k8, k_scale, k8_cache and k_scale_cache go together")
-    _call("dsa_kv8_append", device, stream, _ptr(K), ld_k, _ptr(V), ld_v, _ptr(k8), _ptr(k_scale), _ptr(cu_seqlens),
-          nseq, n, _ptr(seq_lens), _ptr(block_table), max_pages, P, Hkv, D, dI, block, _ptr(k_cache8),
-          _ptr(v_cache8), _ptr(kv_exp), _ptr(k8_cache), _ptr(k_scale_cache))
+    _call("dsa_kv8_append", device, stream, K.data_ptr(), ld_k, V.data_ptr(), ld_v, _ptr(k8), _ptr(k_scale), _ptr(cu_seqlens),
+          nseq, n, seq_lens.data_ptr(), block_table.data_ptr(), max_pages, P, Hkv, D, dI, block, k_cache8.data_ptr(),
+          v_cache8.data_ptr(), kv_exp.data_ptr(), _ptr(k8_cache), _ptr(k_scale_cache))
 
 
 def _kv8_rows(q, idx, k, out, lse, Hkv, D, device):
     """Checks the query-side tensors of an attention call; (rows, Hq)."""
-    if q.dim() != 3:
-        raise ValueError(f"q: expected 3 dims, got shape {tuple(q.shape)}")
-    n, Hq = q.shape[0], q.shape[1]
-    _shaped(q, torch.bfloat16, (n, Hq, D), "q", device)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"q: expected [rows, Hq, {D}], got shape {tuple(shape)}")
+    n, Hq, _ = shape
+    _shaped(q, torch.bfloat16, shape, "q", device)
     if idx is not None:
         _shaped(idx, torch.int32, (n, k), "idx", device)
-    _shaped(out, torch.bfloat16, (n, Hq, D), "out", device)
+    _shaped(out, torch.bfloat16, shape, "out", device)
     if lse is not None:
         _shaped(lse, torch.float32, (n, Hq), "lse", device)
     return n, Hq
@@ -613,13 +625,12 @@ def sparse_gqa_decode_attention_kv8(q, k_cache8, v_cache8, kv_exp, block_table, 
                                     lse=None, stream=None):
     """dsa_sparse_gqa_decode_attention_kv8: attention of each sequence's newest
     token over its selected rows idx [B, k] of the 8-bit cache."""
-    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
-    device = k_cache8.device
+    device, P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
     B, Hq = _kv8_rows(q, idx, int(k), out, lse, Hkv, D, device)
     max_pages = _table(block_table, seq_lens, B, device)
-    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream, _ptr(q), _ptr(k_cache8), _ptr(v_cache8),
-          _ptr(kv_exp), block, _ptr(block_table), max_pages, P, _ptr(seq_lens), _ptr(idx), B, Hq, Hkv, D, int(k),
-          float(sm_scale), _ptr(out), _ptr(lse))
+    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream, q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(),
+          kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), idx.data_ptr(), B, Hq, Hkv, D, int(k),
+          float(sm_scale), out.data_ptr(), _ptr(lse))
 
 
 def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens, idx, cu_seqlens, row_begin, n_rows,
@@ -627,17 +638,16 @@ def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens,
     """dsa_sparse_gqa_prefill_kv8: attention of packed query rows [row_begin,
     row_begin+n_rows), the last tokens of their cached sequences, over their
     selected positions in the 8-bit cache.  Q, O, idx and lse hold these rows."""
-    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
-    device = k_cache8.device
+    device, P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
     n, Hq = _kv8_rows(Q, idx, int(k), O, lse, Hkv, D, device)
     if n != int(n_rows):
         raise ValueError(f"Q: expected {int(n_rows)} rows, got {n}")
     nseq = seq_lens.shape[0]
     max_pages = _table(block_table, seq_lens, nseq, device)
     _shaped(cu_seqlens, torch.int32, (nseq + 1,), "cu_seqlens", device)
-    _call("dsa_sparse_gqa_prefill_kv8", device, stream, _ptr(Q), _ptr(k_cache8), _ptr(v_cache8), _ptr(kv_exp), block,
-          _ptr(block_table), max_pages, P, _ptr(seq_lens), _ptr(idx), _ptr(cu_seqlens), nseq, int(row_begin), n, Hq,
-          Hkv, D, int(k), float(sm_scale), _ptr(O), _ptr(lse))
+    _call("dsa_sparse_gqa_prefill_kv8", device, stream, Q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block,
+          block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), idx.data_ptr(), _ptr(cu_seqlens), nseq, int(row_begin), n, Hq,
+          Hkv, D, int(k), float(sm_scale), O.data_ptr(), _ptr(lse))
 
 
 def decode_kv8_workspace_size(B, max_seq_len, k) -> int:
@@ -649,8 +659,7 @@ def sparse_gqa_decode_kv8(q, q8, q_scale, w, k8_cache, k_scale_cache, k_cache8, 
     """dsa_sparse_gqa_decode_kv8: indexer -> top-k -> attention over the 8-bit
     cache, for one new token per sequence.  ``ws`` is a uint8 CUDA tensor of
     decode_kv8_workspace_size(...) bytes or more."""
-    P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
-    device = k_cache8.device
+    device, P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
     B, Hq = _kv8_rows(q, idx_out, int(k), out, None, Hkv, D, device)
     max_pages = _table(block_table, seq_lens, B, device)
     if q8.dim() != 3:
@@ -661,12 +670,12 @@ def sparse_gqa_decode_kv8(q, q8, q_scale, w, k8_cache, k_scale_cache, k_cache8, 
     _shaped(w, torch.float32, (B, HI), "w", device)
     _shaped(k8_cache, torch.uint8, (P, PAGE_SIZE, dI), "k8_cache", device)
     _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
-    if _device_of(ws, "ws") != device or not ws.is_contiguous():
-        raise ValueError(f"ws: expected a contiguous tensor on {device}")
-    _call("dsa_sparse_gqa_decode_kv8", device, stream, _ptr(q), _ptr(q8), _ptr(q_scale), _ptr(w), _ptr(k8_cache),
-          _ptr(k_scale_cache), _ptr(k_cache8), _ptr(v_cache8), _ptr(kv_exp), block, _ptr(block_table), max_pages, P,
-          _ptr(seq_lens), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k), float(sm_scale), _ptr(ws),
-          ws.numel() * ws.element_size(), _ptr(out), _ptr(idx_out))
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on cuda:{device}")
+    _call("dsa_sparse_gqa_decode_kv8", device, stream, q.data_ptr(), q8.data_ptr(), q_scale.data_ptr(), w.data_ptr(), _ptr(k8_cache),
+          _ptr(k_scale_cache), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P,
+          seq_lens.data_ptr(), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k), float(sm_scale), ws.data_ptr(),
+          ws.nbytes, out.data_ptr(), _ptr(idx_out))
 
 
 # ---------------------------------------------------------------------------
@@ -679,29 +688,31 @@ def _page_bufs(bufs, num_pages, device):
     n = len(bufs)
     bases, sizes = (_P * n)(), (_SZ * n)()
     for i, t in enumerate(bufs):
-        if t.device != device:
-            raise ValueError(f"bufs[{i}]: expected on {device}, got {t.device}")
+        if t.get_device() != device:
+            raise ValueError(f"bufs[{i}]: expected on cuda:{device}, got {t.device}")
         if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
             raise ValueError(f"bufs[{i}]: expected a contiguous tensor of {num_pages} pages, got {tuple(t.shape)}")
         bases[i] = t.data_ptr()
-        sizes[i] = t.numel() // num_pages * t.element_size()
+        sizes[i] = t.nbytes // max(num_pages, 1)
     return bases, sizes, n
 
 
 def _pool(block_table, seq_lens, refcount):
     """Checks a pool's state; (device, n_slots, max_pages, num_pages)."""
     device = _device_of(block_table, "block_table")
-    max_pages = _table(block_table, seq_lens, block_table.shape[0], device)
-    if refcount.dim() != 1:
-        raise ValueError(f"refcount: expected 1 dim, got shape {tuple(refcount.shape)}")
-    _shaped(refcount, torch.int32, (refcount.shape[0],), "refcount", device)
-    return device, block_table.shape[0], max_pages, refcount.shape[0]
+    n_slots, num_pages = seq_lens.numel(), refcount.numel()
+    max_pages = _table(block_table, seq_lens, n_slots, device)
+    _shaped(refcount, torch.int32, (num_pages,), "refcount", device)
+    return device, n_slots, max_pages, num_pages
 
 
-def _entries(device, **lists):
-    n = len(next(iter(lists.values())))
-    for name, t in lists.items():
-        _shaped(t, torch.int32, (n,), name, device)
+def _entries(device, first, second, third=None):
+    """Checks a call's int32 lists (name, tensor) of one length; the length."""
+    n = first[1].numel()
+    _shaped(first[1], torch.int32, (n,), first[0], device)
+    _shaped(second[1], torch.int32, (n,), second[0], device)
+    if third is not None:
+        _shaped(third[1], torch.int32, (n,), third[0], device)
     return n
 
 
@@ -709,9 +720,9 @@ def pages_extend(slots, new_lens, block_table, seq_lens, refcount, status, strea
     """dsa_pages_extend: sequence slots[i] grows to new_lens[i] tokens and gets
     the pages that takes; status[i] = 0, or 1 (no pages left) or 2 (refused)."""
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
-    n = _entries(device, slots=slots, new_lens=new_lens, status=status)
-    _call("dsa_pages_extend", device, stream, _ptr(slots), _ptr(new_lens), n, _ptr(block_table), n_slots, max_pages,
-          _ptr(seq_lens), _ptr(refcount), P, _ptr(status))
+    n = _entries(device, ("slots", slots), ("new_lens", new_lens), ("status", status))
+    _call("dsa_pages_extend", device, stream, slots.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages,
+          seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr())
 
 
 def pages_fork(bufs, parents, children, block_table, seq_lens, refcount, status, stream=None):
@@ -719,19 +730,20 @@ def pages_fork(bufs, parents, children, block_table, seq_lens, refcount, status,
     parents[i]: full pages shared, a partly filled last page copied in every
     buffer of ``bufs`` (tensors [num_pages, ...]); status as in pages_extend."""
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
-    n = _entries(device, parents=parents, children=children, status=status)
+    n = _entries(device, ("parents", parents), ("children", children), ("status", status))
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_fork", device, stream, bases, sizes, n_bufs, _ptr(parents), _ptr(children), n,
-          _ptr(block_table), n_slots, max_pages, _ptr(seq_lens), _ptr(refcount), P, _ptr(status))
+    _call("dsa_pages_fork", device, stream, bases, sizes, n_bufs, parents.data_ptr(), children.data_ptr(), n,
+          block_table.data_ptr(), n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr())
 
 
 def pages_free(slots, block_table, seq_lens, refcount, stream=None):
     """dsa_pages_free: the sequences in ``slots`` become empty and pages that no
     other sequence holds become free."""
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
-    n = _entries(device, slots=slots)
-    _call("dsa_pages_free", device, stream, _ptr(slots), n, _ptr(block_table), n_slots, max_pages, _ptr(seq_lens),
-          _ptr(refcount), P)
+    n = slots.numel()
+    _shaped(slots, torch.int32, (n,), "slots", device)
+    _call("dsa_pages_free", device, stream, slots.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages, seq_lens.data_ptr(),
+          refcount.data_ptr(), P)
 
 
 def pages_copy(bufs, src, dst, stream=None):
@@ -743,9 +755,9 @@ def pages_copy(bufs, src, dst, stream=None):
     if bufs[0].dim() < 1:
         raise ValueError("bufs[0]: expected [num_pages, ...]")
     P = bufs[0].shape[0]
-    n = _entries(device, src=src, dst=dst)
+    n = _entries(device, ("src", src), ("dst", dst))
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_copy", device, stream, bases, sizes, n_bufs, _ptr(src), _ptr(dst), n, P)
+    _call("dsa_pages_copy", device, stream, bases, sizes, n_bufs, src.data_ptr(), dst.data_ptr(), n, P)
 
 
 def pages_compact_workspace_size(num_pages) -> int:
@@ -765,12 +777,12 @@ def pages_compact(bufs, block_table, seq_lens, refcount, page_map, n_used, ws, b
     _shaped(refs_out, torch.int32, (P,), "refcount_out", device)
     _shaped(page_map, torch.int32, (P,), "page_map", device)
     _shaped(n_used, torch.int32, (1,), "n_used", device)
-    if _device_of(ws, "ws") != device or not ws.is_contiguous():
-        raise ValueError(f"ws: expected a contiguous tensor on {device}")
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on cuda:{device}")
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_compact", device, stream, bases, sizes, n_bufs, _ptr(block_table), _ptr(table_out), n_slots,
-          max_pages, _ptr(seq_lens), _ptr(refcount), _ptr(refs_out), P, _ptr(page_map), _ptr(n_used), _ptr(ws),
-          ws.numel() * ws.element_size())
+    _call("dsa_pages_compact", device, stream, bases, sizes, n_bufs, block_table.data_ptr(), table_out.data_ptr(), n_slots,
+          max_pages, seq_lens.data_ptr(), refcount.data_ptr(), refs_out.data_ptr(), P, page_map.data_ptr(), n_used.data_ptr(), ws.data_ptr(),
+          ws.nbytes)
 
 
 class KV8Cache:
