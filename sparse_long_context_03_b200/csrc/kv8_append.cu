@@ -48,14 +48,17 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
     // the unit's sequence and its part of it: block j of those that the
     // sequence's new tokens touch.  Sequence b has the units from
     // cu[b] / block + 2 b on, at least as many as the blocks it touches.
+    // The unit's CTAs (heads, K and V, the indexer's keys) are neighbours:
+    // together they read whole rows.
+    const int per = 2 * a.Hkv + (a.k8 != nullptr ? 1 : 0), part = blockIdx.x % per;
     int b, t0, pos0, n_new, j;
     if (a.cu == nullptr) {
-        b = blockIdx.x;
+        b = blockIdx.x / per;
         t0 = b;
         n_new = 1;
         j = 0;
     } else {
-        const int u = blockIdx.x;
+        const int u = blockIdx.x / per;
         b = warp_find_seq(a.nseq, u, [&](int i) { return __ldg(a.cu + i) / a.block + 2 * i; });
         t0 = __ldg(a.cu + b);
         n_new = __ldg(a.cu + b + 1) - t0;
@@ -69,33 +72,35 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
     const int lo = (int)max(start, (int64_t)pos0);
     const int hi = (int)min(start + a.block, (int64_t)pos0 + n_new);
     if (lo >= hi || start / kPage >= a.max_pages) return;
-    const int page = __ldg(a.block_table + (size_t)b * a.max_pages + start / kPage);
-    if (page < 0 || page >= a.num_pages) return;
     const int m = hi - lo, m_old = lo - (int)start;
     const int64_t tok = t0 + (lo - pos0);           // the first of them among the new tokens
-    const int64_t row = (int64_t)page * kPage + lo % kPage;
-
-    if (blockIdx.y == 2 * a.Hkv) {                  // the indexer's keys
-        const int per = a.dI / 16;
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + tok * a.dI);
-        uint4 *dst = reinterpret_cast<uint4 *>(a.k8_cache + row * a.dI);
-        for (int i = threadIdx.x; i < m * per; i += T) dst[i] = __ldg(src + i);
-        for (int i = threadIdx.x; i < m; i += T) a.k_scale_cache[row + i] = __ldg(a.k_scale + tok + i);
-        return;
-    }
-    const int g = blockIdx.y >> 1, which = blockIdx.y & 1;
-    const uint16_t *src = a.src[which] + tok * a.ld[which] + (size_t)g * D;
-    uint8_t *exp_at = a.exps + (((size_t)page * (kPage / a.block) + (start % kPage) / a.block) * a.Hkv + g) * 2 + which;
-    const int e_old = m_old > 0 ? *exp_at : kKv8ExpMin;
+    // the values are asked for before their page is known
+    const int g = part >> 1, which = part & 1;
+    const bool keys = part == 2 * a.Hkv;
     uint4 x[kMaxVec];
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < kMaxVec; ++i) {
         const int v = threadIdx.x + i * T;
         x[i] = make_uint4(0, 0, 0, 0);
-        if (v < m * VPT)
-            x[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(v / VPT) * a.ld[which]) + v % VPT);
+        if (v < m * VPT && !keys)
+            x[i] = __ldg(reinterpret_cast<const uint4 *>(a.src[which] + (tok + v / VPT) * a.ld[which] + (size_t)g * D) +
+                         v % VPT);
     }
+    const int page = __ldg(a.block_table + (size_t)b * a.max_pages + start / kPage);
+    if (page < 0 || page >= a.num_pages) return;
+    const int64_t row = (int64_t)page * kPage + lo % kPage;
+
+    if (keys) {                                     // the indexer's keys
+        const int n16 = a.dI / 16;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + tok * a.dI);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.k8_cache + row * a.dI);
+        for (int i = threadIdx.x; i < m * n16; i += T) dst[i] = __ldg(src + i);
+        for (int i = threadIdx.x; i < m; i += T) a.k_scale_cache[row + i] = __ldg(a.k_scale + tok + i);
+        return;
+    }
+    uint8_t *exp_at = a.exps + (((size_t)page * (kPage / a.block) + (start % kPage) / a.block) * a.Hkv + g) * 2 + which;
+    const int e_old = m_old > 0 ? *exp_at : kKv8ExpMin;
 #pragma unroll
     for (int i = 0; i < kMaxVec; ++i) {
         mx = abs_max_bf16x2(mx, x[i].x);
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
 // kMaxNew: the most new tokens of one block
 template <int D, int T, int kMaxNew>
 cudaError_t launch(const AppendArgs &a, unsigned units, cudaStream_t stream) {
-    kv8_append_kernel<D, T, kMaxNew><<<dim3(units, 2 * a.Hkv + (a.k8 != nullptr ? 1 : 0)), T, 0, stream>>>(a);
+    kv8_append_kernel<D, T, kMaxNew><<<units * (2 * a.Hkv + (a.k8 != nullptr ? 1 : 0)), T, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -27,6 +27,7 @@ constexpr int kPageTokens = 64;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
+constexpr int kOneCtaPages = 4096;   // pools whose counts one CTA reads alone: one batch of loads
 constexpr int kHash = 2 * kPagesMaxEntries;
 static_assert(kPagesMaxEntries <= kThreads, "one entry per thread");
 
@@ -43,6 +44,27 @@ __device__ __forceinline__ Stretch stretch_of(int num_pages, int warps, int w) {
     const int per = (num_pages + warps * 32 - 1) / (warps * 32) * 32;
     const long long b = (long long)per * w;
     return {(int)min(b, (long long)num_pages), (int)min(b + per, (long long)num_pages)};
+}
+
+// Goes over a stretch's counts in rounds of 32 ids, the loads of kAhead rounds
+// together (a load per step would pay the latency once per round): f(id, count)
+// by every lane, with id >= end (and count -1) past the stretch, while f
+// returns true (the same in every lane).
+constexpr int kAhead = 4;
+template <typename F>
+__device__ __forceinline__ void over_stretch(const int32_t *counts, int begin, int end, F f) {
+    const int lane = threadIdx.x & 31;
+    for (int p0 = begin; p0 < end; p0 += 32 * kAhead) {
+        int c[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int p = p0 + 32 * i + lane;
+            c[i] = p < end ? counts[p] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (p0 + 32 * i < end && !f(p0 + 32 * i + lane, c[i])) return;
+    }
 }
 
 // Sum over the cluster's warps before this one, and over all of them, of a
@@ -158,7 +180,10 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
                                   (int)cluster.block_rank() * kWarps + warp);
     int count = 0;
     if (wanted > 0)
-        for (int p = st.begin + lane; p < st.end; p += 32) count += a.refcount[p] == 0;
+        over_stretch(a.refcount, st.begin, st.end, [&](int, int c) {
+            count += c == 0;
+            return true;
+        });
     count = __reduce_add_sync(0xFFFFFFFFu, count);
     cluster_wait();
     const int2 free = cluster_scan(cluster, scan, count);   // every length has been read behind its barrier
@@ -177,12 +202,11 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
     }
     const int given = lo > 0 ? upto[lo - 1] : 0;
     int rank = free.x;
-    for (int p0 = st.begin; p0 < st.end && rank < given; p0 += 32) {
-        const int p = p0 + lane;
-        const bool is_free = p < st.end && a.refcount[p] == 0;
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, is_free);
+    if (rank >= given) return;
+    over_stretch(a.refcount, st.begin, st.end, [&](int p, int c) {
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, c == 0);
         const int r = rank + __popc(m & ((1u << lane) - 1u));
-        if (is_free && r < given) {
+        if (c == 0 && r < given) {
             int b = 0, e = a.n - 1;                          // the first entry with upto > r
             while (b < e) {
                 const int mid = (b + e) >> 1;
@@ -193,7 +217,8 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
             a.refcount[p] = 1;
         }
         rank += __popc(m);
-    }
+        return rank < given;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -211,7 +236,7 @@ struct PageBufs {
 };
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyBatch = 4;                              // units in flight per thread
+constexpr int kCopyBatch = 2;                              // units in flight per thread
 constexpr int kPiece = kCopyThreads * kCopyBatch;          // units of one piece of a page
 
 template <typename T>
@@ -329,20 +354,25 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
     const Stretch st = stretch_of(a.num_pages, kWarps * C, me * kWarps + warp);
     int count = 0;
-    for (int p = st.begin + lane; p < st.end; p += 32) count += a.refs_in[p] != 0;
+    over_stretch(a.refs_in, st.begin, st.end, [&](int p, int c) {
+        count += p < st.end && c != 0;
+        return true;
+    });
     cluster_wait();
     const int2 used = cluster_scan(cluster, scan0, __reduce_add_sync(0xFFFFFFFFu, count));
     const int n_used = used.y;
     // free ids below n_used, by stretch: their total is the number of moves
     int holes = 0;
-    for (int p = st.begin + lane; p < min(st.end, n_used); p += 32) holes += a.refs_in[p] == 0;
+    if (st.begin < n_used)
+        over_stretch(a.refs_in, st.begin, min(st.end, n_used), [&](int, int c) {
+            holes += c == 0;
+            return true;
+        });
     const int2 low = cluster_scan(cluster, scan1, __reduce_add_sync(0xFFFFFFFFu, holes));
     int lr = low.x, ur = used.x;
     const int below = n_used - low.y;                 // used ids below n_used
-    for (int p0 = st.begin; p0 < st.end; p0 += 32) {
-        const int p = p0 + lane;
+    over_stretch(a.refs_in, st.begin, st.end, [&](int p, int ref) {
         const bool in = p < st.end;
-        const int ref = in ? a.refs_in[p] : 0;
         const unsigned mu = __ballot_sync(0xFFFFFFFFu, in && ref != 0);
         const unsigned ml = __ballot_sync(0xFFFFFFFFu, in && ref == 0 && p < n_used);
         const unsigned before = (1u << lane) - 1u;
@@ -357,17 +387,15 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
         }
         ur += __popc(mu);
         lr += __popc(ml);
-    }
+        return true;
+    });
     cluster.sync();                                   // both lists are complete
     for (int r = me * kThreads + threadIdx.x; r < low.y; r += C * kThreads) {
         const int h = a.highs[r], l = a.lows[r];
-        a.refs_out[l] = a.refs_in[h];
+        a.refs_out[l] = a.refs_in[h];                 // read before it is cleared: the counts may be changed in place
+        a.refs_out[h] = 0;
         a.map[h] = l;
     }
-    // the moved pages' old places, when all their counts have been read (the
-    // counts may be changed in place)
-    cluster.sync();
-    for (int r = me * kThreads + threadIdx.x; r < low.y; r += C * kThreads) a.refs_out[a.highs[r]] = 0;
     if (me == 0 && threadIdx.x == 0) {
         *a.n_used = n_used;
         *a.moves = low.y;
@@ -412,9 +440,7 @@ PageBufs page_bufs(void *const *bases, const size_t *bytes, int n) {
 int pieces_of(const PageBufs &pb) { return pb.units > kPiece ? (pb.units + kPiece - 1) / kPiece : 1; }
 
 cudaLaunchConfig_t cluster_config(int num_pages, cudaLaunchAttribute *attr, cudaStream_t stream) {
-    // one CTA reads the counts of 16K pages in four rounds of loads per warp
-    // lane and less than a second CTA's share of the exchange costs
-    const unsigned ctas = num_pages <= 16384 ? 1 : kMaxCtas;
+    const unsigned ctas = num_pages <= kOneCtaPages ? 1 : kMaxCtas;
     attr->id = cudaLaunchAttributeClusterDimension;
     attr->val.clusterDim.x = ctas;
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
