@@ -384,7 +384,7 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_noalloc(const uint16_t *q,
  *                 exponents of K ([..., 0]) and V ([..., 1]); a cached value
  *                 is e4m3(byte) * 2^(exponent - 127).
  *   scale_block   tokens that share a scale: 16, 32 or 64
- *   num_pages     < 2^25 (a cache row is addressed by 31 bits)
+ *   num_pages     < 2^25 (a cache row is addressed by 31 bits), max_pages too
  *
  * dsa_kv8_append writes new tokens into it.  Sequence b has seq_lens[b]
  * tokens, its new ones included; they are the last of them, and their pages
@@ -399,7 +399,8 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_noalloc(const uint16_t *q,
  * only through those values.
  *
  *   K, V          [n_tokens, Hkv, D] bf16, rows ld_k and ld_v elements apart
- *                 (>= Hkv * D, a multiple of 8; pointers 16-byte aligned)
+ *                 (>= Hkv * D, a multiple of 8; pointers 16-byte aligned, as
+ *                 are the caches'; kv_exp 2-byte)
  *   cu_seqlens    device int32 [nseq + 1]: sequence b's new tokens are rows
  *                 cu_seqlens[b] .. cu_seqlens[b+1]-1 (ascending; empty
  *                 sequences allowed; rows from cu_seqlens[nseq] on are not

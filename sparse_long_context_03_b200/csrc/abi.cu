@@ -387,7 +387,10 @@ dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint16_t *V, 
     const Range range(__func__);
     if (nseq < 0 || n_tokens < 0 || max_pages < 1 || num_pages < 1 || Hkv < 1) return DSA_ERR_INVALID_ARG;
     if (cu_seqlens == nullptr && n_tokens != nseq) return DSA_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128) || Hkv > 1024 || !kv8_cache_supported(num_pages, scale_block) || nseq > (1 << 29))
+    if ((D != 64 && D != 128) || Hkv > 1024 || !kv8_cache_supported(num_pages, scale_block) || max_pages >= (1 << 25))
+        return DSA_ERR_UNSUPPORTED_SHAPE;
+    // units of work (blocks that new tokens may touch) times CTAs of a unit
+    if (((int64_t)n_tokens / scale_block + 2 * (int64_t)nseq) * (Hkv + 1) >= (1ll << 31))
         return DSA_ERR_UNSUPPORTED_SHAPE;
     if (nseq == 0 || n_tokens == 0) return DSA_OK;
     const int given = (k8 != nullptr) + (k_scale != nullptr) + (k8_cache != nullptr) + (k_scale_cache != nullptr);
@@ -397,7 +400,7 @@ dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint16_t *V, 
     if (ld_k < (int64_t)Hkv * D || ld_v < (int64_t)Hkv * D || ld_k % 8 != 0 || ld_v % 8 != 0)
         return DSA_ERR_INVALID_ARG;
     if (!aligned(K, 16) || !aligned(V, 16) || !aligned(k_cache8, 16) || !aligned(v_cache8, 16) || !aligned(k8, 16) ||
-        !aligned(k8_cache, 16) || !aligned(k_scale, 4) || !aligned(k_scale_cache, 4))
+        !aligned(k8_cache, 16) || !aligned(k_scale, 4) || !aligned(k_scale_cache, 4) || !aligned(kv_exp, 2))
         return DSA_ERR_INVALID_ARG;
     return cuda_status(dsa::launch_kv8_append(K, ld_k, V, ld_v, k8, k_scale, cu_seqlens, nseq, n_tokens, seq_lens,
                                               block_table, max_pages, num_pages, Hkv, D, dI, scale_block, k_cache8,

@@ -9,9 +9,9 @@
 // outgrows all before it, and the rewriting rounds only values that become
 // subnormal in e4m3 (the scale is a power of two).
 //
-// Work unit: one CTA per (block of tokens, head, K or V); the block's new
+// Work unit: one CTA per (block of tokens, head), for K and V; the block's new
 // values stay in registers between the maximum and the conversion, so K and V
-// are read once.  One more row of CTAs copies the indexer's keys.  Bound by
+// are read once.  One more CTA per block copies the indexer's keys.  Bound by
 // HBM for prompts (2 bytes in, 1 byte out per value), by latency for single
 // tokens.
 #include "kernels.h"
@@ -27,7 +27,7 @@ struct AppendArgs {
     const uint8_t *k8;
     const float *k_scale;
     const int32_t *cu, *seq_lens, *block_table;
-    int nseq, n_tokens, max_pages, num_pages, Hkv, dI, block;
+    int nseq, n_tokens, max_pages, num_pages, Hkv, dI, shift;   // 2^shift tokens to a block
     uint8_t *dst[2];
     uint8_t *exps;
     uint8_t *k8_cache;
@@ -40,127 +40,136 @@ __device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Eight bf16 values -> e4m3 of value * inv.
+__device__ __forceinline__ uint2 to_e4m3x8(const uint4 &x, float inv) {
+    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+    uint16_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = f32x2_to_e4m3x2(__uint_as_float(in[i] << 16) * inv, __uint_as_float(in[i] & 0xFFFF0000u) * inv);
+    return make_uint2((uint32_t)out[0] | (uint32_t)out[1] << 16, (uint32_t)out[2] | (uint32_t)out[3] << 16);
+}
+
+// Sixteen e4m3 bytes times f (a power of two), rounded again.
+__device__ __forceinline__ uint4 rescale_e4m3x16(uint4 w, float f) {
+    uint32_t *ws = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const float2 lo = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(ws[h] & 0xFFFFu)));
+        const float2 hi = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(ws[h] >> 16)));
+        ws[h] = (uint32_t)f32x2_to_e4m3x2(lo.x * f, lo.y * f) | (uint32_t)f32x2_to_e4m3x2(hi.x * f, hi.y * f) << 16;
+    }
+    return w;
+}
+
 template <int D, int T, int kMaxNew>
 __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int VPT = D / 8;                      // 16-byte pieces of a new token's row
     constexpr int kMaxVec = (kMaxNew * VPT + T - 1) / T;
-    __shared__ uint32_t red[T / 32];
-    // the unit's sequence and its part of it: block j of those that the
+    __shared__ uint32_t red[2][T / 32];
+    // The unit's sequence and its part of it: block j of those that the
     // sequence's new tokens touch.  Sequence b has the units from
-    // cu[b] / block + 2 b on, at least as many as the blocks it touches.
-    // The unit's CTAs (heads, K and V, the indexer's keys) are neighbours:
-    // together they read whole rows.
-    const int per = 2 * a.Hkv + (a.k8 != nullptr ? 1 : 0), part = blockIdx.x % per;
-    int b, t0, pos0, n_new, j;
+    // cu[b] / block + 2 b on, at least as many as the blocks it touches.  The
+    // unit's CTAs (heads, the indexer's keys) are neighbours: together they
+    // read whole rows.
+    const unsigned per = a.Hkv + (a.k8 != nullptr ? 1 : 0), u = blockIdx.x / per;
+    const int g = blockIdx.x - u * per;
+    int b, t0, n_new, j;
     if (a.cu == nullptr) {
-        b = blockIdx.x / per;
-        t0 = b;
+        b = t0 = u;
         n_new = 1;
         j = 0;
     } else {
-        const int u = blockIdx.x / per;
-        b = warp_find_seq(a.nseq, u, [&](int i) { return __ldg(a.cu + i) / a.block + 2 * i; });
+        b = warp_find_seq(a.nseq, u, [&](int i) { return (__ldg(a.cu + i) >> a.shift) + 2 * i; });
         t0 = __ldg(a.cu + b);
         n_new = __ldg(a.cu + b + 1) - t0;
-        j = u - (t0 / a.block + 2 * b);
-        if (t0 < 0 || n_new <= 0 || (int64_t)t0 + n_new > a.n_tokens) return;
+        j = u - ((t0 >> a.shift) + 2 * b);
+        if (t0 < 0 || n_new <= 0 || n_new > a.n_tokens - t0) return;
     }
-    pos0 = __ldg(a.seq_lens + b) - n_new;           // the first new token's position
-    if (pos0 < 0) return;
-    const int blk = pos0 / a.block + j;             // the block within the sequence
-    const int64_t start = (int64_t)blk * a.block;
-    const int lo = (int)max(start, (int64_t)pos0);
-    const int hi = (int)min(start + a.block, (int64_t)pos0 + n_new);
-    if (lo >= hi || start / kPage >= a.max_pages) return;
-    const int m = hi - lo, m_old = lo - (int)start;
-    const int64_t tok = t0 + (lo - pos0);           // the first of them among the new tokens
+    const int pos0 = __ldg(a.seq_lens + b) - n_new; // the first new token's position
+    if (pos0 < 0 || pos0 >= a.max_pages * kPage) return;
+    const int start = ((pos0 >> a.shift) + j) << a.shift;           // the block's first position
+    const int lo = max(start, pos0), hi = min(start + (1 << a.shift), pos0 + n_new);
+    if (lo >= hi || start >= a.max_pages * kPage) return;
+    const int m = hi - lo, m_old = lo - start, tok = t0 + (lo - pos0);  // tok: the first among the new tokens
+    const bool keys = g == a.Hkv;
     // the values are asked for before their page is known
-    const int g = part >> 1, which = part & 1;
-    const bool keys = part == 2 * a.Hkv;
-    uint4 x[kMaxVec];
-    uint32_t mx = 0;
+    uint4 x[2][kMaxVec];
+    uint32_t mx[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kMaxVec; ++i) {
-        const int v = threadIdx.x + i * T;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (v < m * VPT && !keys)
-            x[i] = __ldg(reinterpret_cast<const uint4 *>(a.src[which] + (tok + v / VPT) * a.ld[which] + (size_t)g * D) +
-                         v % VPT);
+    for (int w = 0; w < 2; ++w) {
+        const uint16_t *src = a.src[w] + tok * a.ld[w] + g * D + threadIdx.x % VPT * 8;
+        const int64_t step = a.ld[w] * (T / VPT);
+        src += threadIdx.x / VPT * a.ld[w];
+#pragma unroll
+        for (int i = 0; i < kMaxVec; ++i) {
+            x[w][i] = make_uint4(0, 0, 0, 0);
+            if (!keys && (int)threadIdx.x + i * T < m * VPT) x[w][i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            src += step;
+        }
     }
     const int page = __ldg(a.block_table + (size_t)b * a.max_pages + start / kPage);
     if (page < 0 || page >= a.num_pages) return;
-    const int64_t row = (int64_t)page * kPage + lo % kPage;
+    const int row = page * kPage + lo % kPage;
 
     if (keys) {                                     // the indexer's keys
         const int n16 = a.dI / 16;
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + tok * a.dI);
-        uint4 *dst = reinterpret_cast<uint4 *>(a.k8_cache + row * a.dI);
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + (int64_t)tok * a.dI);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.k8_cache + (int64_t)row * a.dI);
         for (int i = threadIdx.x; i < m * n16; i += T) dst[i] = __ldg(src + i);
         for (int i = threadIdx.x; i < m; i += T) a.k_scale_cache[row + i] = __ldg(a.k_scale + tok + i);
         return;
     }
-    uint8_t *exp_at = a.exps + (((size_t)page * (kPage / a.block) + (start % kPage) / a.block) * a.Hkv + g) * 2 + which;
-    const int e_old = m_old > 0 ? *exp_at : kKv8ExpMin;
+    uint8_t *exp_at = a.exps + (((size_t)page * (kPage >> a.shift) + (start % kPage >> a.shift)) * a.Hkv + g) * 2;
+    const uint16_t e_both = m_old > 0 ? *reinterpret_cast<const uint16_t *>(exp_at) : kKv8ExpMin | kKv8ExpMin << 8;
 #pragma unroll
-    for (int i = 0; i < kMaxVec; ++i) {
-        mx = abs_max_bf16x2(mx, x[i].x);
-        mx = abs_max_bf16x2(mx, x[i].y);
-        mx = abs_max_bf16x2(mx, x[i].z);
-        mx = abs_max_bf16x2(mx, x[i].w);
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int i = 0; i < kMaxVec; ++i) {
+            mx[w] = abs_max_bf16x2(mx[w], x[w][i].x);
+            mx[w] = abs_max_bf16x2(mx[w], x[w][i].y);
+            mx[w] = abs_max_bf16x2(mx[w], x[w][i].z);
+            mx[w] = abs_max_bf16x2(mx[w], x[w][i].w);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx[w] = abs_max_bf16x2(mx[w], __shfl_xor_sync(0xFFFFFFFFu, mx[w], o));
+        if (lane_id() == 0) red[w][threadIdx.x >> 5] = mx[w];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = abs_max_bf16x2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if (lane_id() == 0) red[threadIdx.x >> 5] = mx;
     __syncthreads();
+    int e_new = 0;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) mx = abs_max_bf16x2(mx, red[w]);
-    const float amax = fmaxf(__uint_as_float(mx << 16), __uint_as_float(mx & 0xFFFF0000u));
-    const int e = max(e_old, min(max(exp_byte_for(amax), kKv8ExpMin), kKv8ExpMax));
-    const float inv = exp_byte_scale(254 - e);
-    uint8_t *dst = a.dst[which] + (row * a.Hkv + g) * D;
-    const size_t stride = (size_t)a.Hkv * D;
+    for (int w = 0; w < 2; ++w) {
+        const int e_old = e_both >> (8 * w) & 0xFF;
 #pragma unroll
-    for (int i = 0; i < kMaxVec; ++i) {
-        const int v = threadIdx.x + i * T;
-        if (v < m * VPT) {
-            uint32_t out[2];
-            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < T / 32; ++i) mx[w] = abs_max_bf16x2(mx[w], red[w][i]);
+        const float amax = fmaxf(__uint_as_float(mx[w] << 16), __uint_as_float(mx[w] & 0xFFFF0000u));
+        const int e = max(e_old, min(max(exp_byte_for(amax), kKv8ExpMin), kKv8ExpMax));
+        e_new |= e << (8 * w);
+        const float inv = exp_byte_scale(254 - e);
+        const int stride = a.Hkv * D;
+        uint8_t *dst = a.dst[w] + (int64_t)row * stride + g * D;
+        uint8_t *to = dst + threadIdx.x / VPT * stride + threadIdx.x % VPT * 8;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint16_t p0 = f32x2_to_e4m3x2(__uint_as_float(in[2 * h] << 16) * inv,
-                                                    __uint_as_float(in[2 * h] & 0xFFFF0000u) * inv);
-                const uint16_t p1 = f32x2_to_e4m3x2(__uint_as_float(in[2 * h + 1] << 16) * inv,
-                                                    __uint_as_float(in[2 * h + 1] & 0xFFFF0000u) * inv);
-                out[h] = (uint32_t)p0 | (uint32_t)p1 << 16;
+        for (int i = 0; i < kMaxVec; ++i) {
+            if ((int)threadIdx.x + i * T < m * VPT) *reinterpret_cast<uint2 *>(to) = to_e4m3x8(x[w][i], inv);
+            to += T / VPT * stride;
+        }
+        if (m_old > 0 && e > e_old) {               // the older tokens' bytes to the new scale
+            const int down = e_old - e;
+            const float f = down > -127 ? exp_byte_scale(127 + down) : 0.f;
+            for (int v = threadIdx.x; v < m_old * (D / 16); v += T) {
+                uint4 *p = reinterpret_cast<uint4 *>(dst - (m_old - v / (D / 16)) * stride) + v % (D / 16);
+                *p = rescale_e4m3x16(*p, f);
             }
-            *reinterpret_cast<uint2 *>(dst + (v / VPT) * stride + (v % VPT) * 8) = make_uint2(out[0], out[1]);
         }
     }
-    if (m_old > 0 && e > e_old) {                   // the older tokens' bytes to the new scale
-        const int down = e_old - e;
-        const float f = down > -127 ? exp_byte_scale(127 + down) : 0.f;
-        uint8_t *old = dst - (size_t)m_old * stride;
-        for (int v = threadIdx.x; v < m_old * (D / 16); v += T) {
-            uint4 *p = reinterpret_cast<uint4 *>(old + (v / (D / 16)) * stride) + v % (D / 16);
-            uint4 w = *p;
-            uint32_t *ws = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const float2 lo2 = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(ws[h] & 0xFFFFu)));
-                const float2 hi2 = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(ws[h] >> 16)));
-                ws[h] = (uint32_t)f32x2_to_e4m3x2(lo2.x * f, lo2.y * f) |
-                        (uint32_t)f32x2_to_e4m3x2(hi2.x * f, hi2.y * f) << 16;
-            }
-            *p = w;
-        }
-    }
-    if (threadIdx.x == 0 && (m_old == 0 || e != e_old)) *exp_at = (uint8_t)e;
+    if (threadIdx.x == 0 && (m_old == 0 || e_new != e_both)) *reinterpret_cast<uint16_t *>(exp_at) = (uint16_t)e_new;
 }
 
 // kMaxNew: the most new tokens of one block
 template <int D, int T, int kMaxNew>
 cudaError_t launch(const AppendArgs &a, unsigned units, cudaStream_t stream) {
-    kv8_append_kernel<D, T, kMaxNew><<<units * (2 * a.Hkv + (a.k8 != nullptr ? 1 : 0)), T, 0, stream>>>(a);
+    kv8_append_kernel<D, T, kMaxNew><<<units * (a.Hkv + (a.k8 != nullptr ? 1 : 0)), T, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -173,7 +182,7 @@ cudaError_t launch_kv8_append(const uint16_t *K, int64_t ld_k, const uint16_t *V
                               uint8_t *kv_exp, uint8_t *k8_cache, float *k_scale_cache, cudaStream_t stream) {
     if (nseq == 0 || n_tokens == 0) return cudaSuccess;
     const AppendArgs a{{K, V}, {ld_k, ld_v}, k8, k_scale, cu, seq_lens, block_table, nseq, n_tokens, max_pages,
-                       num_pages, Hkv, dI, scale_block, {k_cache8, v_cache8}, kv_exp, k8_cache, k_scale_cache};
+                       num_pages, Hkv, dI, scale_block == 16 ? 4 : (scale_block == 32 ? 5 : 6), {k_cache8, v_cache8}, kv_exp, k8_cache, k_scale_cache};
     // a single token is 8 or 16 pieces of 16 bytes: two warps; a block of a
     // prompt is up to 1024 of them: eight warps with four pieces a thread
     if (cu == nullptr) return D == 64 ? launch<64, 64, 1>(a, nseq, stream) : launch<128, 64, 1>(a, nseq, stream);

@@ -48,7 +48,8 @@ def append_args(**kw):
     (dict(k8=B), INVALID), (dict(k8=B, ks=B, k8c=B, ksc=B, dI=48), UNSUPPORTED), (dict(K=None), INVALID),
     (dict(V=None), INVALID), (dict(lens=None), INVALID), (dict(table=None), INVALID), (dict(exp=None), INVALID),
     (dict(ld_k=511), INVALID), (dict(ld_v=516), INVALID), (dict(K=B + 8), INVALID), (dict(kc=B + 8), INVALID),
-    (dict(k8=B + 8, ks=B, k8c=B, ksc=B, dI=64), INVALID), (dict(n=0), OK), (dict(nseq=0, n=0), OK),
+    (dict(k8=B + 8, ks=B, k8c=B, ksc=B, dI=64), INVALID), (dict(exp=B + 1), INVALID),
+    (dict(max_pages=1 << 25), UNSUPPORTED), (dict(nseq=2 ** 29), UNSUPPORTED), (dict(n=0), OK), (dict(nseq=0, n=0), OK),
 ])
 def test_append_refusals(lib, kw, want):
     assert lib.dsa_kv8_append(*append_args(**kw)) == want
