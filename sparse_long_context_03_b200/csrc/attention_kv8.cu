@@ -85,22 +85,16 @@ __device__ __forceinline__ void ldg_stream(uint32_t (&r)[4], const uint8_t *p) {
                  : "l"(p));
 }
 
-// What stands for the rows of entries that select nothing: finite values whose
-// weight is zero.
-__device__ const uint4 g_zero_row[8] = {};
-
-// Issues the loads of K or V (`to`, from `base`) of keys half*16 .. +15 of the
-// warp's 32: `row` holds, per lane, the cache row of its key (-1: none);
-// `all`: none is -1.  base points at the lane's quarter of a row.
+// Issues the loads of K or V (`to`, from `base`, the lane's quarter of a row)
+// of keys half*16 .. +15 of the warp's 32: `row` holds, per lane, the cache
+// row of its key.
 template <int D>
-__device__ __forceinline__ void load_half(uint32_t (&to)[2][D / 16], int row, bool all, int half, const uint8_t *base,
+__device__ __forceinline__ void load_half(uint32_t (&to)[2][D / 16], int row, int half, const uint8_t *base,
                                           uint32_t stride, int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = __shfl_sync(0xFFFFFFFFu, row, half * 16 + (lane >> 2) + 8 * i);
-        const uint8_t *p = base + (uint64_t)(uint32_t)r * stride;
-        if (!all && r < 0) p = reinterpret_cast<const uint8_t *>(g_zero_row) + (lane & 3) * (D / 4);
-        ldg_stream(to[i], p);
+        ldg_stream(to[i], base + (uint64_t)(uint32_t)r * stride);
     }
 }
 
@@ -176,32 +170,45 @@ struct KeyScales {
     float ev;
 };
 
-// Multiplies tile t; next_k and next_v issue the loads that take its place, as
-// soon as its registers are read.
+// Attends to the 32 keys in t[0] and t[1]; next_k(i) and next_v(i) issue the
+// loads that take t[i]'s place, as soon as its registers are read.
 template <int D, typename NextK, typename NextV>
-__device__ __forceinline__ void attend_tile(Kv8State<D> &st, Tile<D> &t, const KeyScales &key, int half, int lane,
+__device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], const KeyScales &key, int lane,
                                             NextK next_k, NextV next_v) {
     const int gid = lane >> 2;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    // two chains of products for each tile: half the latency
+    float s[2][4] = {}, odd[2][4] = {};
 #pragma unroll
-    for (int w = 0; w < D / 16; ++w) {
-        const uint32_t x0 = t.k[0][w], x1 = t.k[1][w];
-        mma_f16_16816(s, e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
-                      e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)), st.q[w][0],
-                      st.q[w][1]);
-    }
-    next_k();
-    const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, key.scales, half * 16 + gid);
-    const uint32_t s8 = __shfl_sync(0xFFFFFFFFu, key.scales, half * 16 + gid + 8);
-    const float ev0 = __shfl_sync(0xFFFFFFFFu, key.ev, half * 16 + gid);
-    const float ev8 = __shfl_sync(0xFFFFFFFFu, key.ev, half * 16 + gid + 8);
-    const float k0 = __uint_as_float(s0 & 0xFFFF0000u), k8 = __uint_as_float(s8 & 0xFFFF0000u);
-    const float iv0 = __uint_as_float(s0 << 16), iv8 = __uint_as_float(s8 << 16);
-    float u[4] = {fmaf(s[0], st.c[0] * k0, ev0), fmaf(s[1], st.c[1] * k0, ev0),
-                  fmaf(s[2], st.c[0] * k8, ev8), fmaf(s[3], st.c[1] * k8, ev8)};
-    float d[4] = {u[0] - st.ref[0], u[1] - st.ref[1], u[2] - st.ref[0], u[3] - st.ref[1]};
-    if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > 15.f)) {
-        float mx[2] = {fmaxf(u[0], u[2]), fmaxf(u[1], u[3])};
+    for (int w = 0; w < D / 16; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t x0 = t[i].k[0][w], x1 = t[i].k[1][w];
+            mma_f16_16816(w & 1 ? odd[i] : s[i], e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
+                          e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)), st.q[w][0],
+                          st.q[w][1]);
+        }
+    next_k(0);
+    next_k(1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] += odd[i][j];
+    float u[2][4], iv[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t sc = __shfl_sync(0xFFFFFFFFu, key.scales, 16 * i + 8 * h + gid);
+            const float ev = __shfl_sync(0xFFFFFFFFu, key.ev, 16 * i + 8 * h + gid);
+            const float ks = __uint_as_float(sc & 0xFFFF0000u);
+            iv[i][h] = __uint_as_float(sc << 16);
+            u[i][2 * h] = fmaf(s[i][2 * h], st.c[0] * ks, ev);
+            u[i][2 * h + 1] = fmaf(s[i][2 * h + 1], st.c[1] * ks, ev);
+        }
+    float mx[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmaxf(u[0][i], u[0][2 + i]), fmaxf(u[1][i], u[1][2 + i]));
+    if (__any_sync(0xFFFFFFFFu, fmaxf(mx[0] - st.ref[0], mx[1] - st.ref[1]) > 15.f)) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
@@ -214,8 +221,6 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, Tile<D> &t, const K
             alpha[i] = fast_exp2(st.ref[i] - ref);
             st.ref[i] = ref;
             st.l[i] *= alpha[i];
-            d[i] = u[i] - ref;
-            d[2 + i] = u[2 + i] - ref;
         }
 #pragma unroll
         for (int w = 0; w < D / 16; ++w) {
@@ -225,22 +230,29 @@ __device__ __forceinline__ void attend_tile(Kv8State<D> &st, Tile<D> &t, const K
             st.o[w][3] *= alpha[1];
         }
     }
-    const float p0 = fast_exp2(d[0]), p1 = fast_exp2(d[1]), p2 = fast_exp2(d[2]), p3 = fast_exp2(d[3]);
-    st.l[0] = fmaf(p2, iv8, fmaf(p0, iv0, st.l[0]));
-    st.l[1] = fmaf(p3, iv8, fmaf(p1, iv0, st.l[1]));
-    const uint32_t b0 = movmatrix_trans(pack_f16x2(p0, p1));
-    const uint32_t b1 = movmatrix_trans(pack_f16x2(p2, p3));
-    // a movmatrix takes a pair of dims from a lane per key to a lane per two
-    // keys
+    uint32_t b[2][2];
 #pragma unroll
-    for (int w = 0; w < D / 16; ++w) {
-        const uint32_t x = t.v[0][w], y = t.v[1][w];
-        mma_f16_16816(st.o[w], movmatrix_trans(e4m3x2_to_f16x2((uint16_t)x)),
-                      movmatrix_trans(e4m3x2_to_f16x2((uint16_t)(x >> 16))),
-                      movmatrix_trans(e4m3x2_to_f16x2((uint16_t)y)),
-                      movmatrix_trans(e4m3x2_to_f16x2((uint16_t)(y >> 16))), b0, b1);
-    }
-    next_v();
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float p0 = fast_exp2(u[i][2 * h] - st.ref[0]), p1 = fast_exp2(u[i][2 * h + 1] - st.ref[1]);
+            st.l[0] = fmaf(p0, iv[i][h], st.l[0]);
+            st.l[1] = fmaf(p1, iv[i][h], st.l[1]);
+            b[i][h] = movmatrix_trans(pack_f16x2(p0, p1));
+        }
+    // the transpose takes V from a lane per key to a lane per two keys, two
+    // dims at a time; the byte permute makes pairs of keys of one dim
+#pragma unroll
+    for (int w = 0; w < D / 16; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t x = __byte_perm(movmatrix_trans(t[i].v[0][w]), 0u, 0x3120);
+            const uint32_t y = __byte_perm(movmatrix_trans(t[i].v[1][w]), 0u, 0x3120);
+            mma_f16_16816(st.o[w], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                          e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b[i][0], b[i][1]);
+        }
+    next_v(0);
+    next_v(1);
 }
 
 // Shared memory of a joined pair: a part per warp (its sums), then what the
@@ -307,8 +319,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     // of an index read, the selected position; -1 if it is none
     auto position = [&](int s, int step) { return step * 32 + lane < n_vis && s <= t ? s : -1; };
     auto page_of = [&](int s) { return s >= 0 ? __ldg(bt + s / kPage) : -1; };
-    int row;
-    bool all;
+    int row, some = -1;
     KeyScales key;
     auto resolve = [&](int s, int page) {
         row = -1;
@@ -320,39 +331,44 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
             key.scales = (e & 0xFFu) << 23 | (254u - (e >> 8)) << 7;
             key.ev = (float)(int)(e >> 8) - 127.f;
         }
-        all = __all_sync(0xFFFFFFFFu, row >= 0);
+        // an entry that selects nothing reads a row that another entry
+        // selected, this step's or an earlier one's: with a weight of 0 its
+        // values add nothing, and a NaN in them is the output's anyway
+        const unsigned found = __ballot_sync(0xFFFFFFFFu, row >= 0);
+        if (found != 0) some = __shfl_sync(0xFFFFFFFFu, row, __ffs(found) - 1);
+        if (row < 0) row = some;
     };
     if (C > 1) cluster_arrive();                    // waited for before the first store to another CTA
     Kv8State<D> st;
     clear_sums<D>(st);
-    if (step0 < steps) {
-        Tile<D> tile[2];
-        int s0 = position(first, step0), s1 = position(second, step0 + nw);
+    // the first step that selects anything
+    int step = step0, s0 = position(first, step0);
+    resolve(s0, page_of(s0));
+    while (some < 0 && (step += nw) < steps) {
+        s0 = position(index_at(step), step);
         resolve(s0, page_of(s0));
+    }
+    if (some >= 0) {
+        Tile<D> tile[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            load_half<D>(tile[h].k, row, all, h, kg, stride, lane);
-            load_half<D>(tile[h].v, row, all, h, vg, stride, lane);
-        }
-        s0 = s1;
-        int p0 = page_of(s0);
-        s1 = index_at(step0 + 2 * nw);
+        for (int h = 0; h < 2; ++h) load_half<D>(tile[h].k, row, h, kg, stride, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_half<D>(tile[h].v, row, h, vg, stride, lane);
+        s0 = position(step == step0 ? second : index_at(step + nw), step + nw);
+        int p0 = page_of(s0), s1 = index_at(step + 2 * nw);
         load_q<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
-        for (int step = step0; step < steps; step += nw) {
+        for (; step < steps; step += nw) {
             const KeyScales now = key;
-            // the next step's rows; none behind the last step, whose loads then
-            // read zeros from L1 (a branch around them would make them wait:
-            // 436 us became 752 on a 2048-row prompt chunk)
+            // the next step's rows; behind the last step those of the last (a
+            // branch around the loads would make them wait: 436 us became 752
+            // on a 2048-row prompt chunk)
             resolve(s0, p0);
             s0 = position(s1, step + 2 * nw);
             p0 = page_of(s0);
             s1 = index_at(step + 3 * nw);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                attend_tile<D>(
-                    st, tile[h], now, h, lane,
-                    [&] { load_half<D>(tile[h].k, row, all, h, kg, stride, lane); },
-                    [&] { load_half<D>(tile[h].v, row, all, h, vg, stride, lane); });
+            attend_keys<D>(
+                st, tile, now, lane, [&](int h) { load_half<D>(tile[h].k, row, h, kg, stride, lane); },
+                [&](int h) { load_half<D>(tile[h].v, row, h, vg, stride, lane); });
         }
     }
 #pragma unroll
@@ -361,15 +377,6 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         st.l[1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[1], o);
     }
     const int gid = lane >> 2, tig = lane & 3;
-#pragma unroll
-    for (int w = 0; w < D / 16; ++w)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float x = st.o[w][i], y = st.o[w][2 + i];
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, gid & 1 ? x : y, 4);
-            st.o[w][i] = gid & 1 ? other : x;
-            st.o[w][2 + i] = gid & 1 ? y : other;
-        }
     uint16_t *og = a.out + ((size_t)r * a.Hq + (size_t)g * G) * D;
     float *lg = a.lse != nullptr ? a.lse + (size_t)r * a.Hq + (size_t)g * G : nullptr;
     if (nw == 1) {
