@@ -27,6 +27,12 @@ constexpr int kPageTokens = 64;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
+
+// The second kernel of a call starts while the first one ends: the first lets
+// it, the second waits for the first's results before it touches anything.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 constexpr int kOneCtaPages = 4096;   // pools whose counts one CTA reads alone: one batch of loads
 constexpr int kHash = 2 * kPagesMaxEntries;
 static_assert(kPagesMaxEntries <= kThreads, "one entry per thread");
@@ -120,6 +126,7 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
     __shared__ int warp_sum[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     cluster_arrive();
+    if (FORK) let_next_start();
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
     for (int h = i; h < kHash; h += kThreads) {
@@ -236,7 +243,8 @@ struct PageBufs {
 };
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyBatch = 2;                              // units in flight per thread
+constexpr int kCopyBatch = 4;                              // units in flight per thread
+constexpr int kMoveCtas = 8;                               // CTAs per SM that move pages
 constexpr int kPiece = kCopyThreads * kCopyBatch;          // units of one piece of a page
 
 template <typename T>
@@ -291,6 +299,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 // piece of the page); the first piece's CTA also fills the row.
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_constant__ PageBufs pb,
                                                                   const __grid_constant__ GrantArgs a, int pieces) {
+    wait_for_last();
     const int i = blockIdx.x / pieces, piece = blockIdx.x % pieces;
     if (a.status[i] != kOk) return;
     const int child = __ldg(a.slots + i), parent = __ldg(a.other + i);
@@ -350,6 +359,7 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
     __shared__ ClusterScan scan0, scan1;
     cg::cluster_group cluster = cg::this_cluster();
     cluster_arrive();
+    let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
     const Stretch st = stretch_of(a.num_pages, kWarps * C, me * kWarps + warp);
@@ -402,23 +412,40 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
     }
 }
 
+// The first `remap` CTAs rewrite the block table, the others move pages, the
+// next piece's page ids read ahead.
 __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const __grid_constant__ PageBufs pb,
                                                                   const __grid_constant__ CompactArgs a, int pieces,
                                                                   const int32_t *table_in, int32_t *table_out,
                                                                   const int32_t *seq_lens, int n_slots,
-                                                                  int max_pages) {
-    const long long entries = (long long)n_slots * max_pages;
-    for (long long e = (long long)blockIdx.x * kCopyThreads + threadIdx.x; e < entries;
-         e += (long long)gridDim.x * kCopyThreads) {
-        const int s = (int)(e / max_pages), j = (int)(e % max_pages);
-        const int p = table_in[e];
-        const bool held = j < pages_of(max(__ldg(seq_lens + s), 0)) && p >= 0 && p < a.num_pages;
-        table_out[e] = held ? __ldg(a.map + p) : -1;
+                                                                  int max_pages, int remap) {
+    wait_for_last();
+    if ((int)blockIdx.x < remap) {
+        const long long entries = (long long)n_slots * max_pages;
+        for (long long e = (long long)blockIdx.x * kCopyThreads + threadIdx.x; e < entries;
+             e += (long long)remap * kCopyThreads) {
+            const int s = (int)(e / max_pages), j = (int)(e % max_pages);
+            const int p = table_in[e];
+            const bool held = j < pages_of(max(__ldg(seq_lens + s), 0)) && p >= 0 && p < a.num_pages;
+            table_out[e] = held ? __ldg(a.map + p) : -1;
+        }
+        return;
     }
-    const long long work = (long long)__ldg(a.moves) * pieces;
-    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
-        const int i = (int)(w / pieces);
-        copy_piece(pb, (int)(w % pieces), __ldg(a.highs + i), __ldg(a.lows + i));
+    const long long work = (long long)__ldg(a.moves) * pieces, hop = gridDim.x - remap;
+    long long w = blockIdx.x - remap;
+    int from = 0, to = 0;
+    if (w < work) {
+        from = __ldg(a.highs + w / pieces);
+        to = __ldg(a.lows + w / pieces);
+    }
+    while (w < work) {
+        const int piece = (int)(w % pieces), src = from, dst = to;
+        w += hop;
+        if (w < work) {
+            from = __ldg(a.highs + w / pieces);
+            to = __ldg(a.lows + w / pieces);
+        }
+        copy_piece(pb, piece, src, dst);
     }
 }
 
@@ -453,6 +480,20 @@ cudaLaunchConfig_t cluster_config(int num_pages, cudaLaunchAttribute *attr, cuda
     return cfg;
 }
 
+// The launch of a call's second kernel.
+const cudaLaunchConfig_t *after_config(unsigned grid, cudaLaunchAttribute *attr, cudaLaunchConfig_t *cfg,
+                                       cudaStream_t stream) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    *cfg = {};
+    cfg->gridDim = dim3(grid);
+    cfg->blockDim = dim3(kCopyThreads);
+    cfg->stream = stream;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    return cfg;
+}
+
 }  // namespace
 
 cudaError_t launch_pages_extend(const int32_t *slots, const int32_t *new_lens, int n, int32_t *block_table,
@@ -473,12 +514,12 @@ cudaError_t launch_pages_fork(void *const *bases, const size_t *bytes, int n_buf
     const GrantArgs a{children, parents, n, block_table, n_slots, max_pages, seq_lens, refcount, num_pages, status};
     cudaLaunchAttribute attr{};
     const cudaLaunchConfig_t cfg = cluster_config(num_pages, &attr, stream);
+    cudaLaunchConfig_t cfg2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, pages_grant_kernel<true>, a);
     if (e != cudaSuccess) return e;
     const PageBufs pb = page_bufs(bases, bytes, n_bufs);
     const int pieces = pieces_of(pb);
-    pages_fork_kernel<<<(unsigned)n * pieces, kCopyThreads, 0, stream>>>(pb, a, pieces);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(after_config((unsigned)n * pieces, &attr, &cfg2, stream), pages_fork_kernel, pb, a, pieces);
 }
 
 cudaError_t launch_pages_free(const int32_t *slots, int n, int32_t *block_table, int n_slots, int max_pages,
@@ -510,13 +551,16 @@ cudaError_t launch_pages_compact(void *const *bases, const size_t *bytes, int n_
     const CompactArgs a{refs_in, refs_out, map, n_used, num_pages, w, w + 4, w + 4 + num_pages / 2 + 1};
     cudaLaunchAttribute attr{};
     const cudaLaunchConfig_t cfg = cluster_config(num_pages, &attr, stream);
+    cudaLaunchConfig_t cfg2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, pages_plan_kernel, a);
     if (e != cudaSuccess) return e;
     const PageBufs pb = page_bufs(bases, bytes, n_bufs);
     const int pieces = pieces_of(pb);
-    pages_move_kernel<<<148 * 8, kCopyThreads, 0, stream>>>(pb, a, pieces, table_in, table_out, seq_lens, n_slots,
-                                                            max_pages);
-    return cudaGetLastError();
+    // one table entry per thread up to a wave's worth of CTAs
+    const long long tiles = ((long long)n_slots * max_pages + kCopyThreads - 1) / kCopyThreads;
+    const int remap = (int)(tiles < 148 * 4 ? tiles : 148 * 4);
+    return cudaLaunchKernelEx(after_config(remap + 148 * kMoveCtas, &attr, &cfg2, stream), pages_move_kernel, pb, a,
+                              pieces, table_in, table_out, seq_lens, n_slots, max_pages, remap);
 }
 
 }  // namespace dsa
