@@ -495,9 +495,11 @@ dsa_status_t dsa_sparse_gqa_decode_kv8(const uint16_t *q, const uint8_t *q8, con
         e = dsa::launch_indexer_decode(q8, q_scale, w, k8_cache, k_scale_cache, block_table, max_pages, num_pages,
                                        seq_lens, max_seq_len, B, HI, dI, scores, L.ld, s, keyrange, &have_range);
         if (e != cudaSuccess) return cuda_status(e);
+        e = dsa::launch_topk(scores, L.ld, 0, B, seq_lens, max_seq_len, k, idx, nullptr, base + L.topk_off,
+                             dsa::topk_workspace_bytes(B, max_seq_len, k), s, have_range ? keyrange : nullptr);
+    } else {
+        e = cudaMemsetAsync(idx, 0xFF, (size_t)B * k * sizeof(int32_t), s);  // nothing to select from
     }
-    e = dsa::launch_topk(scores, L.ld, 0, B, seq_lens, max_seq_len, k, idx, nullptr, base + L.topk_off,
-                         dsa::topk_workspace_bytes(B, max_seq_len, k), s, have_range ? keyrange : nullptr);
     if (e != cudaSuccess) return cuda_status(e);
     return cuda_status(dsa::launch_sparse_kv8(q, k_cache8, v_cache8, kv_exp, scale_block, block_table, max_pages,
                                               num_pages, seq_lens, idx, nullptr, 0, 0, B, Hq, Hkv, D, k, sm_scale,

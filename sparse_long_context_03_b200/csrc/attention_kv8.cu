@@ -23,22 +23,32 @@
 // or more exactly; the weights are rounded to fp16 (2^-11, an eighth of what
 // bf16 would lose), the sums are of the unrounded weights.
 //
-// Work unit: one warp owns 16 keys of a (query, KV group) pair at a time, all
+// Work unit: one warp owns 32 keys of a (query, KV group) pair at a time, all
 // G <= 8 heads at once (keys on the matrix M dimension, heads on N = 8).  The
 // selected rows go from global memory straight to registers, a quarter of a
 // row to a lane.  For S = K Q^T any permutation of the head dims is allowed as
 // long as Q has the same, so the lane's bytes are operands as they are; for
-// O^T = V^T P^T the converted pairs of dims pass through a movmatrix each, to
-// the lanes that hold two keys of a dim.  There is no shared-memory stage and
-// no swizzle.
+// O^T = V^T P^T a movmatrix per word takes them, two dims at a time, to the
+// lanes that hold two keys each, and a byte permute pairs the keys.  There is
+// no shared-memory stage and no swizzle: staging rows through shared memory
+// passes every byte through it twice, and a gather alone then stops at 13 TB/s
+// from L2 against 19 TB/s into registers.
+//
+// What bounds it: instructions.  A warp's 32 keys take about 430 of them, half
+// for the conversions, with three warps to a scheduler (the two steps of K and
+// V in flight take 64 of 168 registers).  2048 query rows of a 32K sequence
+// with k = 2048, 32 heads on 4 groups of 128 dims: 414 us, 10.4 TB/s of
+// gathered rows (the bf16 kernel's 2.1 times as many bytes take 555 us for as
+// many rows); 32 sequences decoding: 22 us, 3.1 TB/s from HBM (bf16 with its
+// combine: 33 us).  Tried and slower: half the registers and 16 warps (457
+// us); the index entries looked up once for four groups into shared memory
+// (393 us for the prompt chunk, but 24.3 us for the decode).
 //
 // Pairs are split over several warps, and over the CTAs of a cluster, when
 // there are too few of them to fill the device; the partial results are
 // joined through shared memory (distributed shared memory across a cluster),
 // in a fixed order, in the same launch and without a workspace.
 #include <cooperative_groups.h>
-
-#include <atomic>
 
 #include "kernels.h"
 #include "kv8.cuh"
@@ -58,7 +68,7 @@ struct Kv8Args {
     const uint8_t *kc, *vc;
     const uint16_t *exps;        // [pages, 64 / block, Hkv] pairs: K's byte low, V's high
     const int32_t *block_table, *seq_lens, *idx, *cu;
-    int max_pages, num_pages, nseq, row_begin, n_rows, Hq, Hkv, k, block_shift, group_major;
+    int max_pages, num_pages, nseq, row_begin, n_rows, Hq, Hkv, k, block_shift;
     float scale_log2;
     uint16_t *out;
     float *lse;
@@ -256,8 +266,8 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], co
 }
 
 // Shared memory of a joined pair: a part per warp (its sums), then what the
-// joining of the warps and of the cluster's CTAs takes.  The sums' heads and quarters
-// of a row lie so far apart that the lanes' stores meet no bank twice.
+// joining of the warps and of the cluster's CTAs takes.  The sums' heads and
+// quarters of a row lie so far apart that the lanes' stores meet no bank twice.
 template <int D>
 struct Join {
     static constexpr int kQuarter = D == 128 ? 36 : 16, kHead = D == 128 ? 148 : 66, kWarp = 8 * kHead;
@@ -281,9 +291,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
     const int pair = blockIdx.x / C;
-    const int r = a.group_major ? pair % a.n_rows : pair / a.Hkv;
-    const int g = a.group_major ? pair / a.n_rows : pair % a.Hkv;
-    const int G = a.Hq / a.Hkv;
+    const int r = pair / a.Hkv, g = pair % a.Hkv, G = a.Hq / a.Hkv;
 
     // 32 keys a step, the pair's warps taking steps in turn.  Nothing waits
     // for what it has just asked for: the indices are read three steps ahead,
@@ -469,7 +477,11 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
 }
 
 // How many warps share a pair, and in how many CTAs: enough that the pairs'
-// warps fill the device once, at most one per 32 keys.
+// warps fill the device once, at most one per 32 keys, in as few CTAs as hold
+// them.  Measured at 32 rows of 4 groups, k = 2048 (12 warps to a pair): 2 CTAs
+// of 6 warps 22.7 us, 4 of 3 23.3, 6 of 2 24.2, 8 of 1 26.8; more warps than
+// the device holds: 2 CTAs of 8 29.9.  One row: 8 CTAs of 8 warps 7.6 us, 4 of
+// 8 8.7, 2 of 8 11.2.  Enough rows take one warp each and join nothing.
 struct Split {
     int warps, ctas;
 };
@@ -518,7 +530,7 @@ cudaError_t launch_sparse_kv8(const uint16_t *q, const uint8_t *k_cache8, const 
     if (n_rows == 0) return cudaSuccess;
     const int shift = scale_block == 16 ? 4 : (scale_block == 32 ? 5 : 6);
     const Kv8Args a{q, k_cache8, v_cache8, reinterpret_cast<const uint16_t *>(kv_exp), block_table, seq_lens, idx, cu,
-                    max_pages, num_pages, nseq, row_begin, n_rows, Hq, Hkv, k, shift, 0, sm_scale * kLog2e, out, lse};
+                    max_pages, num_pages, nseq, row_begin, n_rows, Hq, Hkv, k, shift, sm_scale * kLog2e, out, lse};
     return D == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
 }
 
