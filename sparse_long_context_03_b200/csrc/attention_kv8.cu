@@ -34,9 +34,9 @@
 // passes every byte through it twice, and a gather alone then stops at 13 TB/s
 // from L2 against 19 TB/s into registers.
 //
-// What bounds it: instructions.  A warp's 32 keys take about 430 of them, half
-// for the conversions, with three warps to a scheduler (the two steps of K and
-// V in flight take 64 of 168 registers).  2048 query rows of a 32K sequence
+// What bounds it: instructions.  A warp's 32 keys take about 470 of them, half
+// for the conversions, with three warps to a scheduler (the next step's K and
+// V, in flight, take 64 of 168 registers).  2048 query rows of a 32K sequence
 // with k = 2048, 32 heads on 4 groups of 128 dims: 414 us, 10.4 TB/s of
 // gathered rows (the bf16 kernel's 2.1 times as many bytes take 555 us for as
 // many rows); 32 sequences decoding: 22 us, 3.1 TB/s from HBM (bf16 with its
