@@ -427,7 +427,8 @@ DSA_API dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint1
 /* Decode stage 3 over the 8-bit cache: as dsa_sparse_gqa_decode_attention,
  * with the same treatment of index entries, pages and empty rows, and without
  * a workspace (a row's splits are joined on chip).  kv_exp is 2-byte aligned,
- * q and out 16-byte, k_cache8 and v_cache8 32-byte. */
+ * q and out 16-byte, k_cache8 and v_cache8 32-byte.  k <= 2^30.  Cached scale
+ * exponents outside 87..167 give unspecified results. */
 DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_kv8(const uint16_t *q, const uint8_t *k_cache8,
                                                  const uint8_t *v_cache8, const uint8_t *kv_exp, int scale_block,
                                                  const int32_t *block_table, int max_pages, int num_pages,
@@ -507,7 +508,8 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_kv8(const uint16_t *q, const uint8_t 
  *                     are skipped; a page may be the source of several pairs,
  *                     and the destination of one that is no pair's source
  *                     (its bytes are unspecified otherwise).  n any.
- *   dsa_pages_compact brings the n_used pages in use to the ids 0..n_used-1:
+ *   dsa_pages_compact brings the n_used pages in use (count not 0) to the ids
+ *                     0..n_used-1:
  *                     the k-th used page from n_used on moves to the k-th free
  *                     id below it, all others stay.  page_map [num_pages]
  *                     receives each page's new id (-1: it was free), for

@@ -413,7 +413,7 @@ static dsa_status_t check_kv8_attention(const void *q, const void *k_cache8, con
                                         int k, const void *out) {
     if (rows < 0 || k < 1 || Hq < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1) return DSA_ERR_INVALID_ARG;
     if (!dsa::attention_shape_supported(Hq, Hkv, D) || !kv8_cache_supported(num_pages, scale_block) ||
-        max_pages >= (1 << 25))
+        max_pages >= (1 << 25) || k > (1 << 30))
         return DSA_ERR_UNSUPPORTED_SHAPE;
     if ((int64_t)rows * Hkv >= (1ll << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;  // one CTA per (row, group)
     if (rows == 0) return DSA_OK;

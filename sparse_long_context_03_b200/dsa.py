@@ -601,9 +601,9 @@ def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqle
         _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
     elif k_scale is not None or k8_cache is not None or k_scale_cache is not None:
         raise ValueError("k8, k_scale, k8_cache and k_scale_cache go together")
-    _call("dsa_kv8_append", device, stream, K.data_ptr(), ld_k, V.data_ptr(), ld_v, _ptr(k8), _ptr(k_scale), _ptr(cu_seqlens),
-          nseq, n, seq_lens.data_ptr(), block_table.data_ptr(), max_pages, P, Hkv, D, dI, block, k_cache8.data_ptr(),
-          v_cache8.data_ptr(), kv_exp.data_ptr(), _ptr(k8_cache), _ptr(k_scale_cache))
+    _call("dsa_kv8_append", device, stream, K.data_ptr(), ld_k, V.data_ptr(), ld_v, _ptr(k8), _ptr(k_scale),
+          _ptr(cu_seqlens), nseq, n, seq_lens.data_ptr(), block_table.data_ptr(), max_pages, P, Hkv, D, dI, block,
+          k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), _ptr(k8_cache), _ptr(k_scale_cache))
 
 
 def _kv8_rows(q, idx, k, out, lse, Hkv, D, device):
@@ -628,9 +628,9 @@ def sparse_gqa_decode_attention_kv8(q, k_cache8, v_cache8, kv_exp, block_table, 
     device, P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
     B, Hq = _kv8_rows(q, idx, int(k), out, lse, Hkv, D, device)
     max_pages = _table(block_table, seq_lens, B, device)
-    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream, q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(),
-          kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), idx.data_ptr(), B, Hq, Hkv, D, int(k),
-          float(sm_scale), out.data_ptr(), _ptr(lse))
+    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream, q.data_ptr(), k_cache8.data_ptr(),
+          v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(),
+          idx.data_ptr(), B, Hq, Hkv, D, int(k), float(sm_scale), out.data_ptr(), _ptr(lse))
 
 
 def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens, idx, cu_seqlens, row_begin, n_rows,
@@ -645,9 +645,9 @@ def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens,
     nseq = seq_lens.shape[0]
     max_pages = _table(block_table, seq_lens, nseq, device)
     _shaped(cu_seqlens, torch.int32, (nseq + 1,), "cu_seqlens", device)
-    _call("dsa_sparse_gqa_prefill_kv8", device, stream, Q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block,
-          block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), idx.data_ptr(), _ptr(cu_seqlens), nseq, int(row_begin), n, Hq,
-          Hkv, D, int(k), float(sm_scale), O.data_ptr(), _ptr(lse))
+    _call("dsa_sparse_gqa_prefill_kv8", device, stream, Q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(),
+          kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), idx.data_ptr(),
+          _ptr(cu_seqlens), nseq, int(row_begin), n, Hq, Hkv, D, int(k), float(sm_scale), O.data_ptr(), _ptr(lse))
 
 
 def decode_kv8_workspace_size(B, max_seq_len, k) -> int:
@@ -672,10 +672,10 @@ def sparse_gqa_decode_kv8(q, q8, q_scale, w, k8_cache, k_scale_cache, k_cache8, 
     _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
     if ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on cuda:{device}")
-    _call("dsa_sparse_gqa_decode_kv8", device, stream, q.data_ptr(), q8.data_ptr(), q_scale.data_ptr(), w.data_ptr(), _ptr(k8_cache),
-          _ptr(k_scale_cache), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P,
-          seq_lens.data_ptr(), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k), float(sm_scale), ws.data_ptr(),
-          ws.nbytes, out.data_ptr(), _ptr(idx_out))
+    _call("dsa_sparse_gqa_decode_kv8", device, stream, q.data_ptr(), q8.data_ptr(), q_scale.data_ptr(), w.data_ptr(),
+          _ptr(k8_cache), _ptr(k_scale_cache), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block,
+          block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k),
+          float(sm_scale), ws.data_ptr(), ws.nbytes, out.data_ptr(), _ptr(idx_out))
 
 
 # ---------------------------------------------------------------------------
@@ -721,8 +721,8 @@ def pages_extend(slots, new_lens, block_table, seq_lens, refcount, status, strea
     the pages that takes; status[i] = 0, or 1 (no pages left) or 2 (refused)."""
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
     n = _entries(device, ("slots", slots), ("new_lens", new_lens), ("status", status))
-    _call("dsa_pages_extend", device, stream, slots.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages,
-          seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr())
+    _call("dsa_pages_extend", device, stream, slots.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(),
+          n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr())
 
 
 def pages_fork(bufs, parents, children, block_table, seq_lens, refcount, status, stream=None):
@@ -742,8 +742,8 @@ def pages_free(slots, block_table, seq_lens, refcount, stream=None):
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
     n = slots.numel()
     _shaped(slots, torch.int32, (n,), "slots", device)
-    _call("dsa_pages_free", device, stream, slots.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages, seq_lens.data_ptr(),
-          refcount.data_ptr(), P)
+    _call("dsa_pages_free", device, stream, slots.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages,
+          seq_lens.data_ptr(), refcount.data_ptr(), P)
 
 
 def pages_copy(bufs, src, dst, stream=None):
@@ -780,9 +780,9 @@ def pages_compact(bufs, block_table, seq_lens, refcount, page_map, n_used, ws, b
     if ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on cuda:{device}")
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_compact", device, stream, bases, sizes, n_bufs, block_table.data_ptr(), table_out.data_ptr(), n_slots,
-          max_pages, seq_lens.data_ptr(), refcount.data_ptr(), refs_out.data_ptr(), P, page_map.data_ptr(), n_used.data_ptr(), ws.data_ptr(),
-          ws.nbytes)
+    _call("dsa_pages_compact", device, stream, bases, sizes, n_bufs, block_table.data_ptr(), table_out.data_ptr(),
+          n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(), refs_out.data_ptr(), P, page_map.data_ptr(),
+          n_used.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 class KV8Cache:
@@ -792,7 +792,8 @@ class KV8Cache:
 
     The methods call the functions of this module on the current stream.
     ``slots`` is an int32 CUDA tensor of the sequences that take part, in the
-    order of the batch; None means every slot in order."""
+    order of the batch (one out of range takes part as an empty sequence); None
+    means every slot in order."""
 
     def __init__(self, num_pages, n_slots, max_pages, Hkv, D, dI=None, scale_block=64, device="cuda"):
         if scale_block not in (16, 32, 64):
@@ -812,7 +813,9 @@ class KV8Cache:
     def _rows(self, slots):
         if slots is None:
             return self.block_table, self.seq_lens
-        return self.block_table.index_select(0, slots), self.seq_lens.index_select(0, slots)
+        rows = slots.clamp(0, self.seq_lens.numel() - 1)
+        lens = self.seq_lens.index_select(0, rows)
+        return self.block_table.index_select(0, rows), torch.where(rows == slots, lens, torch.zeros_like(lens))
 
     def extend(self, slots, new_lens):
         """pages_extend; the status tensor."""

@@ -433,3 +433,113 @@ def test_decode_chain_is_its_stages():
     dsa.sparse_gqa_decode_kv8(*args, out2)     # its own index rows in the workspace
     torch.cuda.synchronize()
     assert torch.equal(out, out2)
+
+
+def test_decode_chain_with_empty_sequences():
+    cfg = inputs.config(3)
+    rng = np.random.default_rng(19)
+    d = inputs.decode_inputs(cfg, seq_lens=[300, 1, 2100], seed=22, device=DEV)
+    cache = [dev(c) for c in random_cache(d["num_pages"], cfg.Hkv, cfg.D, 64, rng, 112, 118)]
+    for lens, most in (([300, 0, 2100], d["max_seq_len"]), ([0, 0, 0], d["max_seq_len"]), ([0, 0, 0], 0)):
+        ws = torch.empty(dsa.decode_kv8_workspace_size(3, most, cfg.k), dtype=torch.uint8, device=DEV)
+        out = torch.full((3, cfg.Hq, cfg.D), 7.0, dtype=torch.bfloat16, device=DEV)
+        idx = torch.full((3, cfg.k), 7, dtype=torch.int32, device=DEV)
+        ln = dev(np.array(lens), torch.int32)
+        dsa.sparse_gqa_decode_kv8(d["q"], d["q8"], d["sq"], d["w"], d["k8_cache"], d["sk_cache"], *cache,
+                                  d["block_table"], ln, most, cfg.k, cfg.sm_scale, ws, out, idx_out=idx)
+        want, _ = decode(d["q"], cache, d["block_table"], ln, idx, cfg.sm_scale)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        for b, n in enumerate(lens):
+            assert int((idx[b] >= 0).sum()) == min(n, cfg.k)
+            assert n or not out[b].any()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,k,B,n", [(8, 4, 128, 5000, 2, 21000), (8, 1, 64, 64, 3000, 90),
+                                            (16, 16, 128, 40, 300, 70)])
+def test_decode_attention_large_budgets_and_batches(Hq, Hkv, D, k, B, n):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(n // 2, n, B)
+    table, P = deal(lens, rng)
+    kc, vc, exp = random_cache(P, Hkv, D, 32, rng, 118, 124)
+    q, qt = bf16(rng.standard_normal((B, Hq, D)))
+    idx = pick_rows(lens, k, rng)
+    out, lse = decode(qt, [dev(c) for c in (kc, vc, exp)], dev(table), dev(lens, torch.int32), dev(idx), 0.01)
+    rows = np.unique(rng.integers(0, B, 40))
+    want = ref.attention(q[rows], kc, vc, exp, table, idx[rows], rows, lens[rows] - 1, float(np.float32(0.01)))
+    at = torch.from_numpy(rows).to(DEV)
+    check(out[at], lse[at], want)
+
+
+def test_prefill_of_many_sequences():
+    # more sequences than one round of the search covers, most of them empty
+    rng = np.random.default_rng(20)
+    Hq, Hkv, D, block, k = 4, 2, 64, 16, 24
+    new = rng.integers(0, 3, 1300) * (rng.random(1300) < 0.3)
+    old = rng.integers(0, 100, 1300)
+    lens, cu = old + new, np.concatenate([[0], np.cumsum(new)])
+    table, P = deal(lens, rng)
+    kc, vc, exp = random_cache(P, Hkv, D, block, rng, 118, 126)
+    n = int(cu[-1])
+    seq = np.repeat(np.arange(len(new)), new)
+    pos = old[seq] + np.arange(n) - cu[seq]
+    idx = pick_rows(pos + 1, k, rng)
+    q, qt = bf16(rng.standard_normal((n, Hq, D)))
+    O, lse = prefill(qt, [dev(c) for c in (kc, vc, exp)], dev(table), dev(lens, torch.int32), dev(idx),
+                     dev(cu, torch.int32), 0, n, 0.02)
+    check(O, lse, ref.attention(q, kc, vc, exp, table, idx, seq, pos, float(np.float32(0.02))))
+
+
+def test_two_calls_at_once_and_a_repeated_entry():
+    rng = np.random.default_rng(21)
+    lens, Hq, Hkv, D, block, k = [3000, 700], 16, 4, 128, 64, 512
+    table, P = deal(lens, rng)
+    kc, vc, exp = random_cache(P, Hkv, D, block, rng, 118, 124)
+    idx = pick_rows(lens, k, rng)
+    idx[1, 100:200] = idx[1, 7]      # one key a hundred times: counted as often
+    q, qt = bf16(rng.standard_normal((2, Hq, D)))
+    cache, bt, ln, ix = [dev(c) for c in (kc, vc, exp)], dev(table), dev(np.array(lens), torch.int32), dev(idx)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = [(torch.empty(2, Hq, D, dtype=torch.bfloat16, device=DEV), torch.empty(2, Hq, device=DEV)) for _ in streams]
+    for s, (o, l) in zip(streams, outs):
+        s.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            dsa.sparse_gqa_decode_attention_kv8(qt, *cache, bt, ln, ix, k, 0.01, o, l, stream=s)
+    torch.cuda.synchronize()
+    want = ref.attention(q, kc, vc, exp, table, idx, np.arange(2), np.array(lens) - 1, float(np.float32(0.01)))
+    for o, l in outs:
+        check(o, l, want)
+        assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
+
+
+def test_refusals_of_the_binding():
+    kc = torch.zeros(3, 64, 2, 64, dtype=torch.uint8, device=DEV)
+    exp = torch.full((3, 2, 2, 2), 127, dtype=torch.uint8, device=DEV)
+    bt, ln = torch.zeros(2, 3, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    idx = torch.zeros(2, 8, dtype=torch.int32, device=DEV)
+
+    def attend(**kw):
+        a = dict(q=q, k=kc, v=kc, exp=exp, bt=bt, ln=ln, idx=idx, out=torch.empty_like(q))
+        a.update(kw)
+        dsa.sparse_gqa_decode_attention_kv8(a["q"], a["k"], a["v"], a["exp"], a["bt"], a["ln"], a["idx"], 8, 0.1,
+                                            a["out"])
+
+    attend()
+    for kw in (dict(v=kc[:2]), dict(exp=exp[:, :1, :, :1]), dict(idx=idx[:, :7]), dict(bt=bt[:1]), dict(ln=ln.cpu()),
+               dict(q=q[:, :, ::2]), dict(out=q[:1]), dict(exp=torch.cat([exp, exp, exp], 1)), dict(bt=bt[:, ::2])):
+        with pytest.raises(ValueError):
+            attend(**kw)
+    for kw in (dict(q=q.half()), dict(k=kc.to(torch.int8)), dict(idx=idx.long()), dict(ln=ln.float())):
+        with pytest.raises(TypeError):
+            attend(**kw)
+    kv = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        dsa.kv8_append(kv[:1], kv[:1], kc, kc, exp, bt, ln)                      # one token for two sequences
+    with pytest.raises(ValueError):
+        dsa.kv8_append(kv.transpose(1, 2).contiguous().transpose(1, 2), kv, kc, kc, exp, bt, ln)
+    with pytest.raises(ValueError):
+        dsa.kv8_append(kv, kv, kc, kc, exp, bt, ln, k_scale=torch.ones(2, device=DEV))
+    with pytest.raises(dsa.DSAError):
+        dsa.kv8_append(kv.new_zeros(2, 132)[:, 4:].unflatten(1, (2, 64)), kv, kc, kc, exp, bt, ln)  # rows off 16 bytes
+    torch.cuda.synchronize()

@@ -240,6 +240,42 @@ def test_captured_calls_replay():
         assert np.array_equal(st2.cpu().numpy(), w2)
 
 
+def test_lengths_given_as_the_pool_s_own_tensor_and_calls_on_a_stream():
+    b = Both(100, 6, 20, [(32,)], 8)
+    b.extend([0, 1, 4], [100, 700, 1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    slots, st = i32([1, 0, 2]), i32([9, 9, 9])
+    lens = b.pool.lens.copy()
+    # seq_lens[0..2] as the new lengths of slots 1, 0 and 2: 100 < 700 is refused, 700 > 100 is not
+    dsa.pages_extend(slots, b.state[1][:3], *b.state, st, stream=side)
+    dsa.pages_free(i32([4]), *b.state, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    want = b.pool.extend([1, 0, 2], lens[:3])
+    b.pool.free([4])
+    b.same(st, want)
+    assert list(want) == [2, 0, 0]
+
+
+def test_cache_object_takes_slots_out_of_range_as_empty():
+    c = dsa.KV8Cache(20, 3, 4, 2, 64, scale_block=16)
+    good = i32([0, 2])
+    assert not c.extend(good, i32([70, 5])).any()
+    kv = torch.randn(3, 2, 64, device=DEV).to(torch.bfloat16)
+    slots = i32([0, 7, -2])
+    c.append(kv, kv, slots=slots)
+    before = c.k.clone()
+    c.append(kv[1:], kv[1:], slots=slots[1:])     # nothing has a place
+    q = torch.randn(3, 4, 64, device=DEV).to(torch.bfloat16)
+    idx = i32([[69, -1], [0, 1], [0, 1]])
+    out = torch.full_like(q, 3.0)
+    c.prefill(q, idx, i32([0, 1, 2, 3]), out, slots=slots)
+    torch.cuda.synchronize()
+    assert torch.equal(before, c.k) and not out[1:].any() and bool(out[0].any())
+    with pytest.raises(ValueError):
+        c.decode(q, None, None, None, 70, 2, None, out, slots=slots)   # holds no indexer keys
+
+
 def test_a_serving_run_of_them_together():
     """Prompts appended and attended, a sequence forked, single tokens appended
     to all and decoded, one freed, the pool compacted: the forked sequence

@@ -34,6 +34,18 @@ def test_block_exponents():
     assert ref.block_exponent(0.0) == 87 and ref.block_exponent(1e30) == 167
 
 
+def test_a_fallen_scale_rounds_only_what_becomes_subnormal():
+    # bytes written at one scale and moved to a larger one are those written at
+    # the larger one, for every value that is normal there
+    rng = np.random.default_rng(0)
+    x = rng.uniform(-448, 448, 20000) * 2.0 ** rng.integers(-8, 1, 20000)
+    for d in range(1, 9):
+        moved = ref.e4m3_round(ref.e4m3_values(ref.e4m3_round(x)) * 2.0 ** -d)
+        at_once = ref.e4m3_round(x * 2.0 ** -d)
+        normal = np.abs(x) * 2.0 ** -d >= 2.0 ** -6
+        assert normal.any() and np.array_equal(moved[normal], at_once[normal])
+
+
 def append_args(**kw):
     a = dict(K=B, ld_k=512, V=B, ld_v=512, k8=None, ks=None, cu=B, nseq=2, n=5, lens=B, table=B, max_pages=4,
              num_pages=9, Hkv=4, D=128, dI=0, block=64, kc=B, vc=B, exp=B, k8c=None, ksc=None)
@@ -60,7 +72,7 @@ def test_append_refusals(lib, kw, want):
     (dict(D=96), UNSUPPORTED), (dict(block=128), UNSUPPORTED), (dict(num_pages=1 << 25), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(idx=None), INVALID), (dict(out=None), INVALID), (dict(out=B + 8), INVALID),
     (dict(q=B + 2), INVALID), (dict(exp=B + 1), INVALID), (dict(kc=B + 16), INVALID), (dict(vc=B + 16), INVALID), (dict(max_pages=0), INVALID),
-    (dict(n=2 ** 29), UNSUPPORTED), (dict(n=0), OK),
+    (dict(n=2 ** 29), UNSUPPORTED), (dict(k=2 ** 30 + 1), UNSUPPORTED), (dict(n=0), OK),
 ])
 @pytest.mark.parametrize("prefill", [False, True])
 def test_attention_refusals(lib, kw, want, prefill):
