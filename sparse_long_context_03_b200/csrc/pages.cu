@@ -13,12 +13,12 @@
 // over their stretch once more and write the ids.  The entries (at most 1024,
 // one per thread) are worked out by every CTA for itself.  Bound by latency:
 // loads, a barrier across the cluster, loads again.  Freeing 32 sequences and
-// granting their room anew from 13K pages takes 9.8 us; with one CTA and a
+// granting their room anew from 13K pages takes 9.2 us; with one CTA and a
 // load per round of 32 ids it took 20.7.
 //
 // Copying moves pages in pieces of 1024 units, four 16-byte loads in flight to
 // a thread.  2048 pages of 69 KB: 49.8 us, 5.7 TB/s read and written, 88 % of a
-// plain copy's 6.55.  Compacting 720 of 1800 pages: 25.4 us, of which the moved
+// plain copy's 6.55.  Compacting 720 of 1800 pages: 24.9 us, of which the moved
 // bytes' copy would take 15.
 #include <cooperative_groups.h>
 
@@ -61,25 +61,44 @@ __device__ __forceinline__ Stretch stretch_of(int num_pages, int warps, int w) {
     return {(int)min(b, (long long)num_pages), (int)min(b + per, (long long)num_pages)};
 }
 
-// Goes over a stretch's counts in rounds of 32 ids, the loads of kAhead rounds
-// together (a load per step would pay the latency once per round): f(id, count)
-// by every lane, with id >= end (and count -1) past the stretch, while f
-// returns true (the same in every lane).
+// A stretch's counts, gone over several times in rounds of 32 ids, the loads
+// of kAhead rounds together (a load per step would pay the latency once per
+// round).  The first of them stay in registers between the passes.
 constexpr int kAhead = 4;
-template <typename F>
-__device__ __forceinline__ void over_stretch(const int32_t *counts, int begin, int end, F f) {
-    const int lane = threadIdx.x & 31;
-    for (int p0 = begin; p0 < end; p0 += 32 * kAhead) {
-        int c[kAhead];
+struct Counts {
+    const int32_t *counts;
+    int begin, end;
+    int first[kAhead];
+
+    __device__ __forceinline__ void load(int (&c)[kAhead], int p0) const {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int p = p0 + 32 * i + lane;
+            const int p = p0 + 32 * i + (int)(threadIdx.x & 31);
             c[i] = p < end ? counts[p] : -1;
         }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (p0 + 32 * i < end && !f(p0 + 32 * i + lane, c[i])) return;
     }
+    // f(id, count) by every lane, with id >= end past the stretch, while f
+    // returns true (the same in every lane)
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        for (int p0 = begin; p0 < end; p0 += 32 * kAhead) {
+            int c[kAhead];
+            if (p0 == begin) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) c[i] = first[i];
+            } else {
+                load(c, p0);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (p0 + 32 * i < end && !f(p0 + 32 * i + (int)(threadIdx.x & 31), c[i])) return;
+        }
+    }
+};
+__device__ __forceinline__ Counts counts_of(const int32_t *counts, Stretch st) {
+    Counts c{counts, st.begin, st.end, {}};
+    c.load(c.first, st.begin);
+    return c;
 }
 
 // Sum over the cluster's warps before this one, and over all of them, of a
@@ -195,11 +214,14 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
     const Stretch st = stretch_of(a.num_pages, kWarps * (int)cluster.num_blocks(),
                                   (int)cluster.block_rank() * kWarps + warp);
     int count = 0;
-    if (wanted > 0)
-        over_stretch(a.refcount, st.begin, st.end, [&](int, int c) {
+    Counts pages{};
+    if (wanted > 0) {
+        pages = counts_of(a.refcount, st);
+        pages.each([&](int, int c) {
             count += c == 0;
             return true;
         });
+    }
     count = __reduce_add_sync(0xFFFFFFFFu, count);
     cluster_wait();
     const int2 free = cluster_scan(cluster, scan, count);   // every length has been read behind its barrier
@@ -219,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
     const int given = lo > 0 ? upto[lo - 1] : 0;
     int rank = free.x;
     if (rank >= given) return;
-    over_stretch(a.refcount, st.begin, st.end, [&](int p, int c) {
+    pages.each([&](int p, int c) {
         const unsigned m = __ballot_sync(0xFFFFFFFFu, c == 0);
         const int r = rank + __popc(m & ((1u << lane) - 1u));
         if (c == 0 && r < given) {
@@ -373,7 +395,8 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
     const Stretch st = stretch_of(a.num_pages, kWarps * C, me * kWarps + warp);
     int count = 0;
-    over_stretch(a.refs_in, st.begin, st.end, [&](int p, int c) {
+    const Counts pages = counts_of(a.refs_in, st);
+    pages.each([&](int p, int c) {
         count += p < st.end && c != 0;
         return true;
     });
@@ -383,14 +406,14 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
     // free ids below n_used, by stretch: their total is the number of moves
     int holes = 0;
     if (st.begin < n_used)
-        over_stretch(a.refs_in, st.begin, min(st.end, n_used), [&](int, int c) {
-            holes += c == 0;
+        pages.each([&](int p, int c) {
+            holes += p < st.end && p < n_used && c == 0;
             return true;
         });
     const int2 low = cluster_scan(cluster, scan1, __reduce_add_sync(0xFFFFFFFFu, holes));
     int lr = low.x, ur = used.x;
     const int below = n_used - low.y;                 // used ids below n_used
-    over_stretch(a.refs_in, st.begin, st.end, [&](int p, int ref) {
+    pages.each([&](int p, int ref) {
         const bool in = p < st.end;
         const unsigned mu = __ballot_sync(0xFFFFFFFFu, in && ref != 0);
         const unsigned ml = __ballot_sync(0xFFFFFFFFu, in && ref == 0 && p < n_used);
