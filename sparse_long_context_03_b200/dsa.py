@@ -496,6 +496,9 @@ def sparse_gqa_decode_attention_noalloc(q, k_cache, v_cache, block_table, seq_le
 
 KV8_EXP_MIN = 87  # the least scale exponent byte: 2^-40
 
+_C = torch._C
+_U8, _I32, _BF16, _F32 = torch.uint8, torch.int32, torch.bfloat16, torch.float32
+
 
 def _shaped(t, dtype, shape, name, device):
     """``t`` is a dense tensor of this type and shape on CUDA device ``device``."""
@@ -518,15 +521,15 @@ def _device_of(t, name):
     return device
 
 
-def _call(name, device, stream, *args):
+def _call(name, device, stream, args):
     """The entry point, on ``device`` (made current if it is not) and on the
     given stream or that device's current one."""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)  # a tenth of what current_stream() costs
+        stream = _C._cuda_getCurrentRawStream(device)  # a tenth of what current_stream() costs
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     fn = getattr(_lib or lib(), name)
-    if device == torch.cuda.current_device():
+    if device == _C._cuda_getDevice():
         code = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -542,19 +545,19 @@ def _kv8_cache(k_cache8, v_cache8, kv_exp):
     if len(shape) != 4 or shape[1] != PAGE_SIZE:
         raise ValueError(f"k_cache8: expected [num_pages, {PAGE_SIZE}, Hkv, D], got {tuple(shape)}")
     P, _, Hkv, D = shape
-    _shaped(k_cache8, torch.uint8, shape, "k_cache8", device)
-    _shaped(v_cache8, torch.uint8, shape, "v_cache8", device)
+    _shaped(k_cache8, _U8, shape, "k_cache8", device)
+    _shaped(v_cache8, _U8, shape, "v_cache8", device)
     parts = kv_exp.shape[1] if kv_exp.dim() == 4 else 0
     if parts not in (1, 2, 4):
         raise ValueError(f"kv_exp: expected [num_pages, 1, 2 or 4, Hkv, 2], got {tuple(kv_exp.shape)}")
-    _shaped(kv_exp, torch.uint8, (P, parts, Hkv, 2), "kv_exp", device)
+    _shaped(kv_exp, _U8, (P, parts, Hkv, 2), "kv_exp", device)
     return device, P, Hkv, D, PAGE_SIZE // parts
 
 
 def _token_rows(t, n, Hkv, D, name, device):
     """Checks [n, Hkv, D] bf16 rows that may lie apart; the distance in elements."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
     if t.shape != (n, Hkv, D):
         raise ValueError(f"{name}: expected shape {(n, Hkv, D)}, got {tuple(t.shape)}")
     if t.get_device() != device:
@@ -569,8 +572,8 @@ def _table(block_table, seq_lens, n, device):
     shape = block_table.shape
     if len(shape) != 2 or shape[0] != n:
         raise ValueError(f"block_table: expected [{n}, max_pages], got shape {tuple(shape)}")
-    _shaped(block_table, torch.int32, shape, "block_table", device)
-    _shaped(seq_lens, torch.int32, (n,), "seq_lens", device)
+    _shaped(block_table, _I32, shape, "block_table", device)
+    _shaped(seq_lens, _I32, (n,), "seq_lens", device)
     return shape[1]
 
 
@@ -587,7 +590,7 @@ def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqle
     ld_v = _token_rows(V, n, Hkv, D, "V", device)
     max_pages = _table(block_table, seq_lens, nseq, device)
     if cu_seqlens is not None:
-        _shaped(cu_seqlens, torch.int32, (nseq + 1,), "cu_seqlens", device)
+        _shaped(cu_seqlens, _I32, (nseq + 1,), "cu_seqlens", device)
     elif n != nseq:
         raise ValueError(f"K: expected one token for each of {nseq} sequences, got {n}")
     dI = 0
@@ -595,15 +598,16 @@ def kv8_append(K, V, k_cache8, v_cache8, kv_exp, block_table, seq_lens, cu_seqle
         if k_scale is None or k8_cache is None or k_scale_cache is None:
             raise ValueError("k8, k_scale, k8_cache and k_scale_cache go together")
         dI = k8.shape[-1]
-        _shaped(k8, torch.uint8, (n, dI), "k8", device)
-        _shaped(k_scale, torch.float32, (n,), "k_scale", device)
-        _shaped(k8_cache, torch.uint8, (P, PAGE_SIZE, dI), "k8_cache", device)
-        _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
+        _shaped(k8, _U8, (n, dI), "k8", device)
+        _shaped(k_scale, _F32, (n,), "k_scale", device)
+        _shaped(k8_cache, _U8, (P, PAGE_SIZE, dI), "k8_cache", device)
+        _shaped(k_scale_cache, _F32, (P, PAGE_SIZE), "k_scale_cache", device)
     elif k_scale is not None or k8_cache is not None or k_scale_cache is not None:
         raise ValueError("k8, k_scale, k8_cache and k_scale_cache go together")
-    _call("dsa_kv8_append", device, stream, K.data_ptr(), ld_k, V.data_ptr(), ld_v, _ptr(k8), _ptr(k_scale),
-          _ptr(cu_seqlens), nseq, n, seq_lens.data_ptr(), block_table.data_ptr(), max_pages, P, Hkv, D, dI, block,
-          k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), _ptr(k8_cache), _ptr(k_scale_cache))
+    _call("dsa_kv8_append", device, stream,
+          (K.data_ptr(), ld_k, V.data_ptr(), ld_v, _ptr(k8), _ptr(k_scale), _ptr(cu_seqlens), nseq, n,
+           seq_lens.data_ptr(), block_table.data_ptr(), max_pages, P, Hkv, D, dI, block, k_cache8.data_ptr(),
+           v_cache8.data_ptr(), kv_exp.data_ptr(), _ptr(k8_cache), _ptr(k_scale_cache)))
 
 
 def _kv8_rows(q, idx, k, out, lse, Hkv, D, device):
@@ -612,12 +616,12 @@ def _kv8_rows(q, idx, k, out, lse, Hkv, D, device):
     if len(shape) != 3 or shape[2] != D:
         raise ValueError(f"q: expected [rows, Hq, {D}], got shape {tuple(shape)}")
     n, Hq, _ = shape
-    _shaped(q, torch.bfloat16, shape, "q", device)
+    _shaped(q, _BF16, shape, "q", device)
     if idx is not None:
-        _shaped(idx, torch.int32, (n, k), "idx", device)
-    _shaped(out, torch.bfloat16, shape, "out", device)
+        _shaped(idx, _I32, (n, k), "idx", device)
+    _shaped(out, _BF16, shape, "out", device)
     if lse is not None:
-        _shaped(lse, torch.float32, (n, Hq), "lse", device)
+        _shaped(lse, _F32, (n, Hq), "lse", device)
     return n, Hq
 
 
@@ -628,9 +632,10 @@ def sparse_gqa_decode_attention_kv8(q, k_cache8, v_cache8, kv_exp, block_table, 
     device, P, Hkv, D, block = _kv8_cache(k_cache8, v_cache8, kv_exp)
     B, Hq = _kv8_rows(q, idx, int(k), out, lse, Hkv, D, device)
     max_pages = _table(block_table, seq_lens, B, device)
-    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream, q.data_ptr(), k_cache8.data_ptr(),
-          v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(),
-          idx.data_ptr(), B, Hq, Hkv, D, int(k), float(sm_scale), out.data_ptr(), _ptr(lse))
+    _call("dsa_sparse_gqa_decode_attention_kv8", device, stream,
+          (q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(),
+           max_pages, P, seq_lens.data_ptr(), idx.data_ptr(), B, Hq, Hkv, D, int(k), float(sm_scale), out.data_ptr(),
+           _ptr(lse)))
 
 
 def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens, idx, cu_seqlens, row_begin, n_rows,
@@ -644,10 +649,11 @@ def sparse_gqa_prefill_kv8(Q, k_cache8, v_cache8, kv_exp, block_table, seq_lens,
         raise ValueError(f"Q: expected {int(n_rows)} rows, got {n}")
     nseq = seq_lens.shape[0]
     max_pages = _table(block_table, seq_lens, nseq, device)
-    _shaped(cu_seqlens, torch.int32, (nseq + 1,), "cu_seqlens", device)
-    _call("dsa_sparse_gqa_prefill_kv8", device, stream, Q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(),
-          kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), idx.data_ptr(),
-          _ptr(cu_seqlens), nseq, int(row_begin), n, Hq, Hkv, D, int(k), float(sm_scale), O.data_ptr(), _ptr(lse))
+    _shaped(cu_seqlens, _I32, (nseq + 1,), "cu_seqlens", device)
+    _call("dsa_sparse_gqa_prefill_kv8", device, stream,
+          (Q.data_ptr(), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(),
+           max_pages, P, seq_lens.data_ptr(), idx.data_ptr(), _ptr(cu_seqlens), nseq, int(row_begin), n, Hq, Hkv, D,
+           int(k), float(sm_scale), O.data_ptr(), _ptr(lse)))
 
 
 def decode_kv8_workspace_size(B, max_seq_len, k) -> int:
@@ -665,36 +671,42 @@ def sparse_gqa_decode_kv8(q, q8, q_scale, w, k8_cache, k_scale_cache, k_cache8, 
     if q8.dim() != 3:
         raise ValueError(f"q8: expected 3 dims, got shape {tuple(q8.shape)}")
     HI, dI = q8.shape[1], q8.shape[2]
-    _shaped(q8, torch.uint8, (B, HI, dI), "q8", device)
-    _shaped(q_scale, torch.float32, (B,), "q_scale", device)
-    _shaped(w, torch.float32, (B, HI), "w", device)
-    _shaped(k8_cache, torch.uint8, (P, PAGE_SIZE, dI), "k8_cache", device)
-    _shaped(k_scale_cache, torch.float32, (P, PAGE_SIZE), "k_scale_cache", device)
+    _shaped(q8, _U8, (B, HI, dI), "q8", device)
+    _shaped(q_scale, _F32, (B,), "q_scale", device)
+    _shaped(w, _F32, (B, HI), "w", device)
+    _shaped(k8_cache, _U8, (P, PAGE_SIZE, dI), "k8_cache", device)
+    _shaped(k_scale_cache, _F32, (P, PAGE_SIZE), "k_scale_cache", device)
     if ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on cuda:{device}")
-    _call("dsa_sparse_gqa_decode_kv8", device, stream, q.data_ptr(), q8.data_ptr(), q_scale.data_ptr(), w.data_ptr(),
-          _ptr(k8_cache), _ptr(k_scale_cache), k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block,
-          block_table.data_ptr(), max_pages, P, seq_lens.data_ptr(), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k),
-          float(sm_scale), ws.data_ptr(), ws.nbytes, out.data_ptr(), _ptr(idx_out))
+    _call("dsa_sparse_gqa_decode_kv8", device, stream,
+          (q.data_ptr(), q8.data_ptr(), q_scale.data_ptr(), w.data_ptr(), _ptr(k8_cache), _ptr(k_scale_cache),
+           k_cache8.data_ptr(), v_cache8.data_ptr(), kv_exp.data_ptr(), block, block_table.data_ptr(), max_pages, P,
+           seq_lens.data_ptr(), int(max_seq_len), B, Hq, Hkv, D, HI, dI, int(k), float(sm_scale), ws.data_ptr(),
+           ws.nbytes, out.data_ptr(), _ptr(idx_out)))
 
 
 # ---------------------------------------------------------------------------
 # pages of a cache
 # ---------------------------------------------------------------------------
 
+_POINTERS = [_P * n for n in range(9)]
+_SIZES = [_SZ * n for n in range(9)]
+
+
 def _page_bufs(bufs, num_pages, device):
     """Host arrays of the buffers' addresses and page sizes; each buffer is a
     dense tensor [num_pages, ...]."""
     n = len(bufs)
-    bases, sizes = (_P * n)(), (_SZ * n)()
-    for i, t in enumerate(bufs):
-        if t.get_device() != device:
-            raise ValueError(f"bufs[{i}]: expected on cuda:{device}, got {t.device}")
-        if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
-            raise ValueError(f"bufs[{i}]: expected a contiguous tensor of {num_pages} pages, got {tuple(t.shape)}")
-        bases[i] = t.data_ptr()
-        sizes[i] = t.nbytes // max(num_pages, 1)
-    return bases, sizes, n
+    if n > 8 or num_pages < 1:
+        raise ValueError(f"bufs: expected at most 8 buffers of at least one page, got {n} of {num_pages}")
+    bases, sizes = [], []
+    for t in bufs:
+        if t.get_device() != device or t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
+            raise ValueError(f"bufs[{len(bases)}]: expected a contiguous tensor of {num_pages} pages on cuda:{device}, "
+                             f"got {tuple(t.shape)} on {t.device}")
+        bases.append(t.data_ptr())
+        sizes.append(t.nbytes // num_pages)
+    return _POINTERS[n](*bases), _SIZES[n](*sizes), n
 
 
 def _pool(block_table, seq_lens, refcount):
@@ -702,17 +714,17 @@ def _pool(block_table, seq_lens, refcount):
     device = _device_of(block_table, "block_table")
     n_slots, num_pages = seq_lens.numel(), refcount.numel()
     max_pages = _table(block_table, seq_lens, n_slots, device)
-    _shaped(refcount, torch.int32, (num_pages,), "refcount", device)
+    _shaped(refcount, _I32, (num_pages,), "refcount", device)
     return device, n_slots, max_pages, num_pages
 
 
 def _entries(device, first, second, third=None):
     """Checks a call's int32 lists (name, tensor) of one length; the length."""
     n = first[1].numel()
-    _shaped(first[1], torch.int32, (n,), first[0], device)
-    _shaped(second[1], torch.int32, (n,), second[0], device)
+    _shaped(first[1], _I32, (n,), first[0], device)
+    _shaped(second[1], _I32, (n,), second[0], device)
     if third is not None:
-        _shaped(third[1], torch.int32, (n,), third[0], device)
+        _shaped(third[1], _I32, (n,), third[0], device)
     return n
 
 
@@ -721,8 +733,9 @@ def pages_extend(slots, new_lens, block_table, seq_lens, refcount, status, strea
     the pages that takes; status[i] = 0, or 1 (no pages left) or 2 (refused)."""
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
     n = _entries(device, ("slots", slots), ("new_lens", new_lens), ("status", status))
-    _call("dsa_pages_extend", device, stream, slots.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(),
-          n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr())
+    _call("dsa_pages_extend", device, stream,
+          (slots.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages, seq_lens.data_ptr(),
+           refcount.data_ptr(), P, status.data_ptr()))
 
 
 def pages_fork(bufs, parents, children, block_table, seq_lens, refcount, status, stream=None):
@@ -732,8 +745,9 @@ def pages_fork(bufs, parents, children, block_table, seq_lens, refcount, status,
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
     n = _entries(device, ("parents", parents), ("children", children), ("status", status))
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_fork", device, stream, bases, sizes, n_bufs, parents.data_ptr(), children.data_ptr(), n,
-          block_table.data_ptr(), n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr())
+    _call("dsa_pages_fork", device, stream,
+          (bases, sizes, n_bufs, parents.data_ptr(), children.data_ptr(), n, block_table.data_ptr(), n_slots,
+           max_pages, seq_lens.data_ptr(), refcount.data_ptr(), P, status.data_ptr()))
 
 
 def pages_free(slots, block_table, seq_lens, refcount, stream=None):
@@ -741,9 +755,10 @@ def pages_free(slots, block_table, seq_lens, refcount, stream=None):
     other sequence holds become free."""
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
     n = slots.numel()
-    _shaped(slots, torch.int32, (n,), "slots", device)
-    _call("dsa_pages_free", device, stream, slots.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages,
-          seq_lens.data_ptr(), refcount.data_ptr(), P)
+    _shaped(slots, _I32, (n,), "slots", device)
+    _call("dsa_pages_free", device, stream,
+          (slots.data_ptr(), n, block_table.data_ptr(), n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(),
+           P))
 
 
 def pages_copy(bufs, src, dst, stream=None):
@@ -757,7 +772,8 @@ def pages_copy(bufs, src, dst, stream=None):
     P = bufs[0].shape[0]
     n = _entries(device, ("src", src), ("dst", dst))
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_copy", device, stream, bases, sizes, n_bufs, src.data_ptr(), dst.data_ptr(), n, P)
+    _call("dsa_pages_copy", device, stream,
+          (bases, sizes, n_bufs, src.data_ptr(), dst.data_ptr(), n, P))
 
 
 def pages_compact_workspace_size(num_pages) -> int:
@@ -773,16 +789,17 @@ def pages_compact(bufs, block_table, seq_lens, refcount, page_map, n_used, ws, b
     device, n_slots, max_pages, P = _pool(block_table, seq_lens, refcount)
     table_out = block_table if block_table_out is None else block_table_out
     refs_out = refcount if refcount_out is None else refcount_out
-    _shaped(table_out, torch.int32, (n_slots, max_pages), "block_table_out", device)
-    _shaped(refs_out, torch.int32, (P,), "refcount_out", device)
-    _shaped(page_map, torch.int32, (P,), "page_map", device)
-    _shaped(n_used, torch.int32, (1,), "n_used", device)
+    _shaped(table_out, _I32, (n_slots, max_pages), "block_table_out", device)
+    _shaped(refs_out, _I32, (P,), "refcount_out", device)
+    _shaped(page_map, _I32, (P,), "page_map", device)
+    _shaped(n_used, _I32, (1,), "n_used", device)
     if ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on cuda:{device}")
     bases, sizes, n_bufs = _page_bufs(bufs, P, device)
-    _call("dsa_pages_compact", device, stream, bases, sizes, n_bufs, block_table.data_ptr(), table_out.data_ptr(),
-          n_slots, max_pages, seq_lens.data_ptr(), refcount.data_ptr(), refs_out.data_ptr(), P, page_map.data_ptr(),
-          n_used.data_ptr(), ws.data_ptr(), ws.nbytes)
+    _call("dsa_pages_compact", device, stream,
+          (bases, sizes, n_bufs, block_table.data_ptr(), table_out.data_ptr(), n_slots, max_pages,
+           seq_lens.data_ptr(), refcount.data_ptr(), refs_out.data_ptr(), P, page_map.data_ptr(), n_used.data_ptr(),
+           ws.data_ptr(), ws.nbytes))
 
 
 class KV8Cache:
