@@ -34,20 +34,15 @@
 // passes every byte through it twice, and a gather alone then stops at 13 TB/s
 // from L2 against 19 TB/s into registers.
 //
-// What bounds it: instructions.  A warp's 32 keys take about 470 of them, half
+// What bounds it: instructions.  A warp's 32 keys take about 430 of them, half
 // for the conversions, with three warps to a scheduler (the next step's K and
 // V, in flight, take 64 of 168 registers).  2048 query rows of a 32K sequence
-// with k = 2048, 32 heads on 4 groups of 128 dims: 414 us, 10.4 TB/s of
-// gathered rows (the bf16 kernel's 2.1 times as many bytes take 555 us for as
+// with k = 2048, 32 heads on 4 groups of 128 dims: 391 us, 11.0 TB/s of
+// gathered rows (the bf16 kernel's 2 times as many bytes take 555 us for as
 // many rows); 32 sequences decoding: 22 us, 3.1 TB/s from HBM (bf16 with its
 // combine: 33 us).  Tried and slower: half the registers and 16 warps (457
-// us); the index entries looked up once for four groups into shared memory
-// (393 us for the prompt chunk, but 24.3 us for the decode).
+// us); the rows of later steps asked into L2 beforehand (decode 26.7 us).
 //
-// Pairs are split over several warps, and over the CTAs of a cluster, when
-// there are too few of them to fill the device; the partial results are
-// joined through shared memory (distributed shared memory across a cluster),
-// in a fixed order, in the same launch and without a workspace.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -179,13 +174,18 @@ struct KeyScales {
     uint32_t scales;
     float ev;
 };
+__device__ __forceinline__ KeyScales no_key() { return {0x3F800000u, -INFINITY}; }
+// Of a pair of scale bytes, K's low.
+__device__ __forceinline__ KeyScales key_scales(uint32_t e) {
+    return {(e & 0xFFu) << 23 | (254u - (e >> 8)) << 7, (float)(int)(e >> 8) - 127.f};
+}
 
-// Attends to the 32 keys in t[0] and t[1]; next_k(i) and next_v(i) issue the
-// loads that take t[i]'s place, as soon as its registers are read.
-template <int D, typename NextK, typename NextV>
-__device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], const KeyScales &key, int lane,
-                                            NextK next_k, NextV next_v) {
-    const int gid = lane >> 2;
+// Attends to the 32 keys in t[0] and t[1]; scales(i, h) are those of the
+// lane's key gid + 8 h of t[i], next_k(i) and next_v(i) issue the loads that
+// take t[i]'s place, as soon as its registers are read.
+template <int D, typename Scales, typename NextK, typename NextV>
+__device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Scales scales, NextK next_k,
+                                            NextV next_v) {
     // two chains of products for each tile: half the latency
     float s[2][4] = {}, odd[2][4] = {};
 #pragma unroll
@@ -208,12 +208,11 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], co
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t sc = __shfl_sync(0xFFFFFFFFu, key.scales, 16 * i + 8 * h + gid);
-            const float ev = __shfl_sync(0xFFFFFFFFu, key.ev, 16 * i + 8 * h + gid);
-            const float ks = __uint_as_float(sc & 0xFFFF0000u);
-            iv[i][h] = __uint_as_float(sc << 16);
-            u[i][2 * h] = fmaf(s[i][2 * h], st.c[0] * ks, ev);
-            u[i][2 * h + 1] = fmaf(s[i][2 * h + 1], st.c[1] * ks, ev);
+            const KeyScales x = scales(i, h);
+            const float ks = __uint_as_float(x.scales & 0xFFFF0000u);
+            iv[i][h] = __uint_as_float(x.scales << 16);
+            u[i][2 * h] = fmaf(s[i][2 * h], st.c[0] * ks, x.ev);
+            u[i][2 * h + 1] = fmaf(s[i][2 * h + 1], st.c[1] * ks, x.ev);
         }
     float mx[2];
 #pragma unroll
@@ -265,6 +264,49 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], co
     next_v(1);
 }
 
+// The sequence b and the position t of query row r; false for a row outside
+// every sequence, which is left as it is.
+__device__ __forceinline__ bool query_place(const Kv8Args &a, int r, int &b, int &t) {
+    if (a.cu == nullptr) {
+        b = r;
+        t = __ldg(a.seq_lens + b) - 1;
+    } else {
+        const int rr = a.row_begin + r;
+        if (rr < __ldg(a.cu) || rr >= __ldg(a.cu + a.nseq)) return false;
+        b = warp_find_seq(a.nseq, rr, [&](int i) { return __ldg(a.cu + i); });
+        t = __ldg(a.seq_lens + b) - __ldg(a.cu + b + 1) + rr;
+    }
+    t = min(t, a.max_pages * kPage - 1);
+    return true;
+}
+
+// Sums l over the lanes of a head.
+template <int D>
+__device__ __forceinline__ void sum_weights(Kv8State<D> &st) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        st.l[0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[0], o);
+        st.l[1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[1], o);
+    }
+}
+
+// One warp's result for a pair: og and lg are its group's outputs.
+template <int D>
+__device__ __forceinline__ void write_pair(const Kv8State<D> &st, int G, uint16_t *og, float *lg, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int h = 2 * tig + i;
+        if (h >= G) continue;
+        const float inv = st.l[i] > 0.f ? 1.f / st.l[i] : 0.f;
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w)
+            *reinterpret_cast<uint32_t *>(og + (size_t)h * D + dim_of<D>(gid, w)) =
+                pack_bf16x2(st.o[w][i] * inv, st.o[w][2 + i] * inv);
+        if (lg != nullptr && gid == 0) lg[h] = st.l[i] > 0.f ? (st.ref[i] + __log2f(st.l[i])) * kLn2 : -INFINITY;
+    }
+}
+
 // Shared memory of a joined pair: a part per warp (its sums), then what the
 // joining of the warps and of the cluster's CTAs takes.  The sums' heads and
 // quarters of a row lie so far apart that the lanes' stores meet no bank twice.
@@ -306,19 +348,8 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     };
     const int first = index_at(step0), second = index_at(step0 + nw);
 
-    // the query's sequence b and position t; rows outside every sequence are
-    // left as they are (the same answer in every CTA of a cluster)
     int b, t;
-    if (a.cu == nullptr) {
-        b = r;
-        t = __ldg(a.seq_lens + b) - 1;
-    } else {
-        const int rr = a.row_begin + r;
-        if (rr < __ldg(a.cu) || rr >= __ldg(a.cu + a.nseq)) return;
-        b = warp_find_seq(a.nseq, rr, [&](int i) { return __ldg(a.cu + i); });
-        t = __ldg(a.seq_lens + b) - __ldg(a.cu + b + 1) + rr;
-    }
-    t = min(t, a.max_pages * kPage - 1);
+    if (!query_place(a, r, b, t)) return;           // the same answer in every CTA of a cluster
     const int n_vis = max(min(a.k, t + 1), 0);
     const int32_t *bt = a.block_table + (size_t)b * a.max_pages;
     const uint8_t *kg = a.kc + (size_t)g * D + (lane & 3) * (D / 4), *vg = a.vc + (size_t)g * D + (lane & 3) * (D / 4);
@@ -331,13 +362,10 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     KeyScales key;
     auto resolve = [&](int s, int page) {
         row = -1;
-        key = {0x3F800000u, -INFINITY};
+        key = no_key();
         if (page >= 0 && page < a.num_pages) {
             row = page * kPage + s % kPage;
-            const uint32_t e = __ldg(a.exps + ((size_t)page * (kPage >> a.block_shift) +
-                                               ((s % kPage) >> a.block_shift)) * a.Hkv + g);
-            key.scales = (e & 0xFFu) << 23 | (254u - (e >> 8)) << 7;
-            key.ev = (float)(int)(e >> 8) - 127.f;
+            key = key_scales(__ldg(a.exps + (size_t)(row >> a.block_shift) * a.Hkv + g));
         }
         // an entry that selects nothing reads a row that another entry
         // selected, this step's or an earlier one's: with a weight of 0 its
@@ -375,30 +403,22 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
             p0 = page_of(s0);
             s1 = index_at(step + 3 * nw);
             attend_keys<D>(
-                st, tile, now, lane, [&](int h) { load_half<D>(tile[h].k, row, h, kg, stride, lane); },
+                st, tile,
+                [&](int i, int h) {
+                    const int from = 16 * i + 8 * h + (lane >> 2);
+                    return KeyScales{__shfl_sync(0xFFFFFFFFu, now.scales, from),
+                                     __shfl_sync(0xFFFFFFFFu, now.ev, from)};
+                },
+                [&](int h) { load_half<D>(tile[h].k, row, h, kg, stride, lane); },
                 [&](int h) { load_half<D>(tile[h].v, row, h, vg, stride, lane); });
         }
     }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        st.l[0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[0], o);
-        st.l[1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[1], o);
-    }
+    sum_weights<D>(st);
     const int gid = lane >> 2, tig = lane & 3;
     uint16_t *og = a.out + ((size_t)r * a.Hq + (size_t)g * G) * D;
     float *lg = a.lse != nullptr ? a.lse + (size_t)r * a.Hq + (size_t)g * G : nullptr;
     if (nw == 1) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int h = 2 * tig + i;
-            if (h >= G) continue;
-            const float inv = st.l[i] > 0.f ? 1.f / st.l[i] : 0.f;
-#pragma unroll
-            for (int w = 0; w < D / 16; ++w)
-                *reinterpret_cast<uint32_t *>(og + (size_t)h * D + dim_of<D>(gid, w)) =
-                    pack_bf16x2(st.o[w][i] * inv, st.o[w][2 + i] * inv);
-            if (lg != nullptr && gid == 0) lg[h] = st.l[i] > 0.f ? (st.ref[i] + __log2f(st.l[i])) * kLn2 : -INFINITY;
-        }
+        write_pair<D>(st, G, og, lg, lane);
         return;
     }
     // join the warps' sums: within the CTA, then across the cluster
@@ -476,6 +496,90 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     }
 }
 
+// Where every pair has one warp: a CTA has the pairs of a query's neighbouring
+// groups, one warp each, and looks the query's entries up once for all of
+// them, a block of entries at a time, into shared memory: the rows, and the
+// scales of each group.  Against a warp that looks up for itself this saves 45
+// of 470 instructions per 32 keys, and pays with a block's start, where nothing
+// is under way: 2048 rows (see the head of the file) take 391 us against 420,
+// but 32 rows that are split 24.3 against 22.1, so those keep to
+// sparse_kv8_kernel.  Blocks of 512 entries: 402 us, 1536: 399, 2048: 413.
+constexpr int kBlockKeys = 1024;
+constexpr int kMaxGroups = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(const __grid_constant__ Kv8Args a, int block) {
+    extern __shared__ __align__(16) int rows[];     // [block], then the scales, [groups][block]
+    __shared__ int some_row[kMaxGroups];
+    const int lane = lane_id(), warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+    const int groups = blockDim.x >> 5, per_row = a.Hkv / groups;
+    const int r = blockIdx.x / per_row, g0 = blockIdx.x % per_row * groups, g = g0 + warp, G = a.Hq / a.Hkv;
+    KeyScales *scales = reinterpret_cast<KeyScales *>(rows + block);
+    int b, t;
+    if (!query_place(a, r, b, t)) return;
+    const int n_vis = max(min(a.k, t + 1), 0);
+    const int32_t *idx_row = a.idx + (size_t)r * a.k, *bt = a.block_table + (size_t)b * a.max_pages;
+    const uint32_t stride = (uint32_t)a.Hkv * D;
+    const uint8_t *kg = a.kc + (size_t)g * D + tig * (D / 4), *vg = a.vc + (size_t)g * D + tig * (D / 4);
+    Kv8State<D> st;
+    clear_sums<D>(st);
+    load_q<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
+
+    for (int base = 0; base < n_vis; base += block) {
+        const int n = (min(block, n_vis - base) + 31) / 32 * 32;
+        if (base > 0) __syncthreads();              // the last block's keys are no longer read
+        int some = -1;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            const int s = base + i < n_vis ? __ldg(idx_row + base + i) : -1;
+            const int page = s >= 0 && s <= t ? __ldg(bt + s / kPage) : -1;
+            const bool there = page >= 0 && page < a.num_pages;
+            const int row = there ? page * kPage + s % kPage : -1;
+            rows[i] = row;
+            some = max(some, row);
+            for (int j = 0; j < groups; ++j)
+                scales[j * block + i] =
+                    there ? key_scales(__ldg(a.exps + (size_t)(row >> a.block_shift) * a.Hkv + g0 + j)) : no_key();
+        }
+        some = __reduce_max_sync(0xFFFFFFFFu, some);
+        if (lane == 0) some_row[warp] = some;
+        __syncthreads();
+        for (int w = 0; w < groups; ++w) some = max(some, some_row[w]);
+        if (some < 0) continue;                     // nothing is selected here
+
+        // an entry that selects nothing, and the steps behind the last, read a
+        // row that is selected, as in sparse_kv8_kernel
+        auto row_at = [&](int i) {
+            const int x = i < n ? rows[i] : -1;
+            return x < 0 ? some : x;
+        };
+        auto load = [&](uint32_t(&to)[2][D / 16], const int(&from)[2], const uint8_t *base) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ldg_stream(to[h], base + (uint64_t)(uint32_t)from[h] * stride);
+        };
+        const KeyScales *mine = scales + warp * block + gid;
+        Tile<D> tile[2];
+        int next[2][2];                             // the rows of a step, read before they are needed
+        auto look = [&](int at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) next[i / 2][i % 2] = row_at(at + 8 * i + gid);
+        };
+        look(0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load(tile[i].k, next[i], kg);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load(tile[i].v, next[i], vg);
+        for (int at = 0; at < n; at += 32) {
+            look(at + 32);
+            attend_keys<D>(
+                st, tile, [&](int i, int h) { return mine[at + 16 * i + 8 * h]; },
+                [&](int i) { load(tile[i].k, next[i], kg); }, [&](int i) { load(tile[i].v, next[i], vg); });
+        }
+    }
+    sum_weights<D>(st);
+    const size_t head = (size_t)r * a.Hq + (size_t)g * G;
+    write_pair<D>(st, G, a.out + head * D, a.lse != nullptr ? a.lse + head : nullptr, lane);
+}
+
 // How many warps share a pair, and in how many CTAs: enough that the pairs'
 // warps fill the device once, at most one per 32 keys, in as few CTAs as hold
 // them.  Measured at 32 rows of 4 groups, k = 2048 (12 warps to a pair): 2 CTAs
@@ -501,6 +605,15 @@ cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
     constexpr int kSlots = 148 * 12;  // SMs x warps that the registers of a lane allow
     const int64_t pairs = (int64_t)a.n_rows * a.Hkv;
     const Split sp = split_of(pairs, a.k, kSlots);
+    int groups = a.Hkv < kMaxGroups ? a.Hkv : kMaxGroups;
+    while (a.Hkv % groups != 0) --groups;
+    if (sp.warps * sp.ctas == 1 && groups > 1) {
+        const int block = a.k < kBlockKeys ? (a.k + 31) / 32 * 32 : kBlockKeys;
+        const size_t smem = block * (sizeof(int) + groups * sizeof(KeyScales));
+        static_assert(kBlockKeys * (sizeof(int) + kMaxGroups * sizeof(KeyScales)) <= 48 << 10, "as below");
+        sparse_kv8_rows_kernel<D><<<(unsigned)(pairs / groups), groups * 32, smem, stream>>>(a, block);
+        return cudaGetLastError();
+    }
     const size_t smem = Join<D>::bytes(sp.warps, sp.ctas, a.Hq / a.Hkv);
     static_assert(kMaxWarps * (Join<D>::kWarp + 24) * sizeof(float) + 8 * (D / 2 + 8 + kMaxCluster) * sizeof(float2) <= 48 << 10,
                   "within the default limit of dynamic shared memory");

@@ -471,6 +471,41 @@ def test_decode_attention_large_budgets_and_batches(Hq, Hkv, D, k, B, n):
     check(out[at], lse[at], want)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (6, 3, 128), (32, 4, 128), (8, 8, 64), (5, 5, 128)])
+def test_prefill_of_many_rows(Hq, Hkv, D):
+    # enough rows for one warp to a pair, more entries than a block of the
+    # lookup, and among them blocks and rows that select nothing, entries out
+    # of range and pages outside the pool
+    rng = np.random.default_rng(Hkv)
+    old, new, k, block = 2600, 1000, 2100, 32
+    lens, cu = np.array([old + new]), np.array([0, new])
+    table, P = deal(lens, rng)
+    table[0, 7] = P + 1
+    kc, vc, exp = random_cache(P, Hkv, D, block, rng, 118, 124)
+    spare = np.setdiff1d(np.arange(P), table[0])
+    kc[spare], vc[spare], exp[spare] = 0x7F, 0x7F, 255       # pages that nobody selects
+    pos = old + np.arange(new)
+    idx = pick_rows(pos + 1, k, rng)
+    idx[::7, ::5] = -1
+    idx[1::7, :1024] = 2 ** 31 - 1                            # a block of nothing, then a block of something
+    idx[2::7, 1024:] = -3
+    idx[3::50] = -1
+    idx[4::50] = 7 * 64 + 5                                   # the page that is none
+    q, qt = bf16(rng.standard_normal((new, Hq, D)))
+    O, lse = prefill(qt, [dev(c) for c in (kc, vc, exp)], dev(table), dev(lens, torch.int32), dev(idx),
+                     dev(cu, torch.int32), 0, new, 0.01)
+    rows = np.unique(np.concatenate([np.arange(8), [53, 54, 999], rng.integers(0, new, 12)]))
+    want = ref.attention(q[rows], kc, vc, exp, table, idx[rows], np.zeros(len(rows), int), pos[rows],
+                         float(np.float32(0.01)))
+    at = torch.from_numpy(rows).to(DEV)
+    check(O[at], lse[at], want)
+    assert not O[3::50].any() and not O[4::50].any()
+    assert bool(torch.isfinite(O).all())
+    O2, l2 = prefill(qt, [dev(c) for c in (kc, vc, exp)], dev(table), dev(lens, torch.int32), dev(idx),
+                     dev(cu, torch.int32), 0, new, 0.01)
+    assert torch.equal(O, O2) and torch.equal(lse, l2)
+
+
 def test_prefill_of_many_sequences():
     # more sequences than one round of the search covers, most of them empty
     rng = np.random.default_rng(20)
