@@ -39,9 +39,11 @@
 // V, in flight, take 64 of 168 registers).  2048 query rows of a 32K sequence
 // with k = 2048, 32 heads on 4 groups of 128 dims: 391 us, 11.0 TB/s of
 // gathered rows (the bf16 kernel's 2 times as many bytes take 555 us for as
-// many rows); 32 sequences decoding: 22 us, 3.1 TB/s from HBM (bf16 with its
+// many rows); 32 sequences decoding: 21.5 us, 3.2 TB/s from HBM (bf16 with its
 // combine: 33 us).  Tried and slower: half the registers and 16 warps (457
-// us); the rows of later steps asked into L2 beforehand (decode 26.7 us).
+// us); the rows of later steps asked into L2 beforehand (decode 26.7 us);
+// the next step's products with K among this step's with V (464 us: what is
+// loaded then has less time to come).
 //
 #include <cooperative_groups.h>
 
@@ -182,23 +184,24 @@ __device__ __forceinline__ KeyScales key_scales(uint32_t e) {
 
 // Attends to the 32 keys in t[0] and t[1]; scales(i, h) are those of the
 // lane's key gid + 8 h of t[i], next_k(i) and next_v(i) issue the loads that
-// take t[i]'s place, as soon as its registers are read.
+// take t[i]'s place, as soon as its registers are read (after both tiles: 22.1
+// us against 21.5 for 32 sequences decoding).
 template <int D, typename Scales, typename NextK, typename NextV>
 __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Scales scales, NextK next_k,
                                             NextV next_v) {
     // two chains of products for each tile: half the latency
     float s[2][4] = {}, odd[2][4] = {};
 #pragma unroll
-    for (int w = 0; w < D / 16; ++w)
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int w = 0; w < D / 16; ++w) {
             const uint32_t x0 = t[i].k[0][w], x1 = t[i].k[1][w];
             mma_f16_16816(w & 1 ? odd[i] : s[i], e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
                           e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)), st.q[w][0],
                           st.q[w][1]);
         }
-    next_k(0);
-    next_k(1);
+        next_k(i);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -252,16 +255,16 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Sc
     // the transpose takes V from a lane per key to a lane per two keys, two
     // dims at a time; the byte permute makes pairs of keys of one dim
 #pragma unroll
-    for (int w = 0; w < D / 16; ++w)
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int w = 0; w < D / 16; ++w) {
             const uint32_t x = __byte_perm(movmatrix_trans(t[i].v[0][w]), 0u, 0x3120);
             const uint32_t y = __byte_perm(movmatrix_trans(t[i].v[1][w]), 0u, 0x3120);
             mma_f16_16816(st.o[w], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
                           e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b[i][0], b[i][1]);
         }
-    next_v(0);
-    next_v(1);
+        next_v(i);
+    }
 }
 
 // The sequence b and the position t of query row r; false for a row outside
