@@ -82,12 +82,12 @@ struct Tile {
 // lanes of a key then read its whole row, which costs the fewest passes
 // through L1.
 __device__ __forceinline__ void ldg_stream(uint32_t (&r)[8], const uint8_t *p) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
 }
 __device__ __forceinline__ void ldg_stream(uint32_t (&r)[4], const uint8_t *p) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "l"(p));
 }
@@ -142,7 +142,7 @@ __device__ __forceinline__ void load_q(Kv8State<D> &st, const uint16_t *qg, int 
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         raw[j] = make_uint4(0, 0, 0, 0);
-        if (gid < G) raw[j] = __ldg(reinterpret_cast<const uint4 *>(qg + (size_t)gid * D + tig * (D / 4)) + j);
+        if (gid < G) raw[j] = reinterpret_cast<const uint4 *>(qg + (size_t)gid * D + tig * (D / 4))[j];
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -272,12 +272,12 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Sc
 __device__ __forceinline__ bool query_place(const Kv8Args &a, int r, int &b, int &t) {
     if (a.cu == nullptr) {
         b = r;
-        t = __ldg(a.seq_lens + b) - 1;
+        t = a.seq_lens[b] - 1;
     } else {
         const int rr = a.row_begin + r;
-        if (rr < __ldg(a.cu) || rr >= __ldg(a.cu + a.nseq)) return false;
-        b = warp_find_seq(a.nseq, rr, [&](int i) { return __ldg(a.cu + i); });
-        t = __ldg(a.seq_lens + b) - __ldg(a.cu + b + 1) + rr;
+        if (rr < *a.cu || rr >= a.cu[a.nseq]) return false;
+        b = warp_find_seq(a.nseq, rr, [&](int i) { return a.cu[i]; });
+        t = a.seq_lens[b] - a.cu[b + 1] + rr;
     }
     t = min(t, a.max_pages * kPage - 1);
     return true;
@@ -332,6 +332,7 @@ template <int D>
 __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constant__ Kv8Args a) {
     extern __shared__ __align__(16) float smem[];
     using S = Join<D>;
+    wait_for_last();
     const int lane = lane_id(), warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), crank = (int)cluster.block_rank();
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     const int step0 = crank * W + warp, nw = C * W;
     auto index_at = [&](int step) {
         const int e = step * 32 + lane;
-        return e < a.k ? __ldg(idx_row + e) : -1;
+        return e < a.k ? idx_row[e] : -1;
     };
     const int first = index_at(step0), second = index_at(step0 + nw);
 
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     const int steps = (n_vis + 31) / 32;
     // of an index read, the selected position; -1 if it is none
     auto position = [&](int s, int step) { return step * 32 + lane < n_vis && s <= t ? s : -1; };
-    auto page_of = [&](int s) { return s >= 0 ? __ldg(bt + s / kPage) : -1; };
+    auto page_of = [&](int s) { return s >= 0 ? bt[s / kPage] : -1; };
     int row, some = -1;
     KeyScales key;
     auto resolve = [&](int s, int page) {
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         key = no_key();
         if (page >= 0 && page < a.num_pages) {
             row = page * kPage + s % kPage;
-            key = key_scales(__ldg(a.exps + (size_t)(row >> a.block_shift) * a.Hkv + g));
+            key = key_scales(a.exps[(size_t)(row >> a.block_shift) * a.Hkv + g]);
         }
         // an entry that selects nothing reads a row that another entry
         // selected, this step's or an earlier one's: with a weight of 0 its
@@ -514,6 +515,7 @@ template <int D>
 __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(const __grid_constant__ Kv8Args a, int block) {
     extern __shared__ __align__(16) int rows[];     // [block], then the scales, [groups][block]
     __shared__ int some_row[kMaxGroups];
+    wait_for_last();
     const int lane = lane_id(), warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
     const int groups = blockDim.x >> 5, per_row = a.Hkv / groups;
     const int r = blockIdx.x / per_row, g0 = blockIdx.x % per_row * groups, g = g0 + warp, G = a.Hq / a.Hkv;
@@ -533,15 +535,15 @@ __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(con
         if (base > 0) __syncthreads();              // the last block's keys are no longer read
         int some = -1;
         for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const int s = base + i < n_vis ? __ldg(idx_row + base + i) : -1;
-            const int page = s >= 0 && s <= t ? __ldg(bt + s / kPage) : -1;
+            const int s = base + i < n_vis ? idx_row[base + i] : -1;
+            const int page = s >= 0 && s <= t ? bt[s / kPage] : -1;
             const bool there = page >= 0 && page < a.num_pages;
             const int row = there ? page * kPage + s % kPage : -1;
             rows[i] = row;
             some = max(some, row);
             for (int j = 0; j < groups; ++j)
                 scales[j * block + i] =
-                    there ? key_scales(__ldg(a.exps + (size_t)(row >> a.block_shift) * a.Hkv + g0 + j)) : no_key();
+                    there ? key_scales(a.exps[(size_t)(row >> a.block_shift) * a.Hkv + g0 + j]) : no_key();
         }
         some = __reduce_max_sync(0xFFFFFFFFu, some);
         if (lane == 0) some_row[warp] = some;
@@ -614,26 +616,15 @@ cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
         const int block = a.k < kBlockKeys ? (a.k + 31) / 32 * 32 : kBlockKeys;
         const size_t smem = block * (sizeof(int) + groups * sizeof(KeyScales));
         static_assert(kBlockKeys * (sizeof(int) + kMaxGroups * sizeof(KeyScales)) <= 48 << 10, "as below");
-        sparse_kv8_rows_kernel<D><<<(unsigned)(pairs / groups), groups * 32, smem, stream>>>(a, block);
-        return cudaGetLastError();
+        return EarlyLaunch((unsigned)(pairs / groups), groups * 32, smem, stream)(sparse_kv8_rows_kernel<D>, a, block);
     }
     const size_t smem = Join<D>::bytes(sp.warps, sp.ctas, a.Hq / a.Hkv);
     static_assert(kMaxWarps * (Join<D>::kWarp + 24) * sizeof(float) + 8 * (D / 2 + 8 + kMaxCluster) * sizeof(float2) <= 48 << 10,
                   "within the default limit of dynamic shared memory");
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)sp.ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(pairs * sp.ctas));
-    cfg.blockDim = dim3(sp.warps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    // only where it is needed: an SM holds 8 CTAs of a cluster launch, even of
-    // clusters of one, but 12 one-warp CTAs of a plain one
-    cfg.attrs = &attr;
-    cfg.numAttrs = sp.ctas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, sparse_kv8_kernel<D>, a);
+    // a cluster only where it is needed: an SM holds 8 CTAs of a cluster launch,
+    // even of clusters of one, but 12 one-warp CTAs of a plain one
+    return EarlyLaunch((unsigned)(pairs * sp.ctas), sp.warps * 32, smem, stream,
+                       sp.ctas > 1 ? sp.ctas : 0)(sparse_kv8_kernel<D>, a);
 }
 
 }  // namespace

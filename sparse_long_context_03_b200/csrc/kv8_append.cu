@@ -13,10 +13,10 @@
 // values stay in registers between the maximum and the conversion, so K and V
 // are read once.  One more CTA per block copies the indexer's keys.  Bound by
 // HBM for prompts (2 bytes in, 1 byte out per value): a 32K prompt of 4 heads
-// of 128 takes 20.5 us, 5.1 TB/s, against 16 us for a plain copy of as many
+// of 128 takes 20.3 us, 5.1 TB/s, against 16 us for a plain copy of as many
 // bytes.  (K and V in CTAs of their own, with divisions in place of shifts,
 // took 27.6 us: more instructions than the loads could hide.)  Single tokens
-// are bound by the chain of loads length, page, scale: 2.0 us for 32 sequences.
+// are bound by the chain of loads length, page, scale: 1.8 us for 32 sequences.
 #include "kernels.h"
 #include "kv8.cuh"
 
@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
     constexpr int VPT = D / 8;                      // 16-byte pieces of a new token's row
     constexpr int kMaxVec = (kMaxNew * VPT + T - 1) / T;
     __shared__ uint32_t red[2][T / 32];
+    wait_for_last();
     // The unit's sequence and its part of it: block j of those that the
     // sequence's new tokens touch.  Sequence b has the units from
     // cu[b] / block + 2 b on, at least as many as the blocks it touches.  The
@@ -83,13 +84,13 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
         n_new = 1;
         j = 0;
     } else {
-        b = warp_find_seq(a.nseq, u, [&](int i) { return (__ldg(a.cu + i) >> a.shift) + 2 * i; });
-        t0 = __ldg(a.cu + b);
-        n_new = __ldg(a.cu + b + 1) - t0;
+        b = warp_find_seq(a.nseq, u, [&](int i) { return (a.cu[i] >> a.shift) + 2 * i; });
+        t0 = a.cu[b];
+        n_new = a.cu[b + 1] - t0;
         j = u - ((t0 >> a.shift) + 2 * b);
         if (t0 < 0 || n_new <= 0 || n_new > a.n_tokens - t0) return;
     }
-    const int pos0 = __ldg(a.seq_lens + b) - n_new; // the first new token's position
+    const int pos0 = a.seq_lens[b] - n_new; // the first new token's position
     if (pos0 < 0 || pos0 >= a.max_pages * kPage) return;
     const int start = ((pos0 >> a.shift) + j) << a.shift;           // the block's first position
     const int lo = max(start, pos0), hi = min(start + (1 << a.shift), pos0 + n_new);
@@ -107,11 +108,11 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
 #pragma unroll
         for (int i = 0; i < kMaxVec; ++i) {
             x[w][i] = make_uint4(0, 0, 0, 0);
-            if (!keys && (int)threadIdx.x + i * T < m * VPT) x[w][i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            if (!keys && (int)threadIdx.x + i * T < m * VPT) x[w][i] = *reinterpret_cast<const uint4 *>(src);
             src += step;
         }
     }
-    const int page = __ldg(a.block_table + (size_t)b * a.max_pages + start / kPage);
+    const int page = a.block_table[(size_t)b * a.max_pages + start / kPage];
     if (page < 0 || page >= a.num_pages) return;
     const int row = page * kPage + lo % kPage;
 
@@ -119,8 +120,8 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
         const int n16 = a.dI / 16;
         const uint4 *src = reinterpret_cast<const uint4 *>(a.k8 + (int64_t)tok * a.dI);
         uint4 *dst = reinterpret_cast<uint4 *>(a.k8_cache + (int64_t)row * a.dI);
-        for (int i = threadIdx.x; i < m * n16; i += T) dst[i] = __ldg(src + i);
-        for (int i = threadIdx.x; i < m; i += T) a.k_scale_cache[row + i] = __ldg(a.k_scale + tok + i);
+        for (int i = threadIdx.x; i < m * n16; i += T) dst[i] = src[i];
+        for (int i = threadIdx.x; i < m; i += T) a.k_scale_cache[row + i] = a.k_scale[tok + i];
         return;
     }
     uint8_t *exp_at = a.exps + (((size_t)page * (kPage >> a.shift) + (start % kPage >> a.shift)) * a.Hkv + g) * 2;
@@ -172,8 +173,7 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
 // kMaxNew: the most new tokens of one block
 template <int D, int T, int kMaxNew>
 cudaError_t launch(const AppendArgs &a, unsigned units, cudaStream_t stream) {
-    kv8_append_kernel<D, T, kMaxNew><<<units * (a.Hkv + (a.k8 != nullptr ? 1 : 0)), T, 0, stream>>>(a);
-    return cudaGetLastError();
+    return EarlyLaunch(units * (a.Hkv + (a.k8 != nullptr ? 1 : 0)), T, 0, stream)(kv8_append_kernel<D, T, kMaxNew>, a);
 }
 
 }  // namespace

@@ -13,11 +13,11 @@
 // over their stretch once more and write the ids.  The entries (at most 1024,
 // one per thread) are worked out by every CTA for itself.  Bound by latency:
 // loads, a barrier across the cluster, loads again.  Freeing 32 sequences and
-// granting their room anew from 13K pages takes 9.2 us; with one CTA and a
+// granting their room anew from 13K pages takes 8.5 us; with one CTA and a
 // load per round of 32 ids it took 20.7.
 //
 // Copying moves pages in pieces of 1024 units, four 16-byte loads in flight to
-// a thread.  2048 pages of 69 KB: 49.8 us, 5.7 TB/s read and written, 88 % of a
+// a thread.  2048 pages of 69 KB: 49.4 us, 5.7 TB/s read and written, 88 % of a
 // plain copy's 6.55.  Compacting 720 of 1800 pages: 24.9 us, of which the moved
 // bytes' copy would take 15.
 #include <cooperative_groups.h>
@@ -35,11 +35,6 @@ constexpr int kPageTokens = 64;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
-
-// The second kernel of a call starts while the first one ends: the first lets
-// it, the second waits for the first's results before it touches anything.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // Pools whose counts one CTA reads alone: one batch of loads, and no exchange.
 constexpr int kOneCtaPages = 4096;
@@ -155,6 +150,7 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
     cg::cluster_group cluster = cg::this_cluster();
     cluster_arrive();
     if (FORK) let_next_start();
+    wait_for_last();
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
     for (int h = i; h < kHash; h += kThreads) {
@@ -165,16 +161,16 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
     int s = -1, len = 0, to = 0, need = 0, place = 0;
     bool bad = true;
     if (i < a.n) {
-        s = __ldg(a.slots + i);
+        s = a.slots[i];
         bad = s < 0 || s >= a.n_slots;
         if (!bad) {
             len = a.seq_lens[s];
             if (FORK) {
-                const int p = __ldg(a.other + i);
+                const int p = a.other[i];
                 bad = p < 0 || p >= a.n_slots || len != 0;
                 if (!bad) to = a.seq_lens[p];
             } else {
-                to = __ldg(a.other + i);
+                to = a.other[i];
             }
             bad = bad || len < 0 || to < len || (long long)to > (long long)a.max_pages * kPageTokens;
             // the first entry that names a slot has it; a later one is refused
@@ -280,7 +276,7 @@ constexpr int kPiece = kCopyThreads * kCopyBatch;          // units of one piece
 
 template <typename T>
 __device__ __forceinline__ void move_unit(const char *s, char *d) {
-    *reinterpret_cast<T *>(d) = __ldg(reinterpret_cast<const T *>(s));
+    *reinterpret_cast<T *>(d) = *reinterpret_cast<const T *>(s);
 }
 
 // Piece `piece` of page src to page dst by one CTA.
@@ -298,7 +294,7 @@ __device__ __forceinline__ void copy_piece(const PageBufs &pb, int piece, int sr
         const char *s = pb.base[b] + (size_t)src * pb.page_bytes[b] + off;
         char *d = pb.base[b] + (size_t)dst * pb.page_bytes[b] + off;
         if (pb.shift[b] == 4) {
-            x[i] = __ldg(reinterpret_cast<const uint4 *>(s));
+            x[i] = *reinterpret_cast<const uint4 *>(s);
             to[i] = d;
         } else if (pb.shift[b] == 3) {
             move_unit<uint2>(s, d);
@@ -318,9 +314,10 @@ __device__ __forceinline__ void copy_piece(const PageBufs &pb, int piece, int sr
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PageBufs pb,
                                                                   const int32_t *src, const int32_t *dst, int n,
                                                                   int pieces, int num_pages) {
+    wait_for_last();
     for (long long w = blockIdx.x; w < (long long)n * pieces; w += gridDim.x) {
         const int i = (int)(w / pieces);
-        const int s = __ldg(src + i), d = __ldg(dst + i);
+        const int s = src[i], d = dst[i];
         if (s < 0 || s >= num_pages || d < 0 || d >= num_pages || s == d) continue;
         copy_piece(pb, (int)(w % pieces), s, d);
     }
@@ -333,7 +330,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_c
     wait_for_last();
     const int i = blockIdx.x / pieces, piece = blockIdx.x % pieces;
     if (a.status[i] != kOk) return;
-    const int child = __ldg(a.slots + i), parent = __ldg(a.other + i);
+    const int child = a.slots[i], parent = a.other[i];
     const int len = a.seq_lens[child], full = len / kPageTokens;
     if (child == parent) return;                              // an empty sequence forked to itself
     const int32_t *from = a.block_table + (size_t)parent * a.max_pages;
@@ -355,10 +352,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_c
 __global__ void __launch_bounds__(256) pages_free_kernel(const int32_t *slots, int n, int32_t *block_table,
                                                          int n_slots, int max_pages, int32_t *seq_lens,
                                                          int32_t *refcount, int num_pages) {
-    const int i = blockIdx.x, s = __ldg(slots + i);
+    wait_for_last();
+    const int i = blockIdx.x, s = slots[i];
     if (s < 0 || s >= n_slots) return;
     bool again = false;
-    for (int j = threadIdx.x; j < i; j += blockDim.x) again = again || __ldg(slots + j) == s;
+    for (int j = threadIdx.x; j < i; j += blockDim.x) again = again || slots[j] == s;
     if (__syncthreads_or(again)) return;
     const int len = seq_lens[s];
     __syncthreads();
@@ -391,6 +389,7 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const __grid_const
     cg::cluster_group cluster = cg::this_cluster();
     cluster_arrive();
     let_next_start();
+    wait_for_last();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
     const Stretch st = stretch_of(a.num_pages, kWarps * C, me * kWarps + warp);
@@ -458,24 +457,24 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const __grid_c
              e += (long long)remap * kCopyThreads) {
             const int s = (int)(e / max_pages), j = (int)(e % max_pages);
             const int p = table_in[e];
-            const bool held = j < pages_of(max(__ldg(seq_lens + s), 0)) && p >= 0 && p < a.num_pages;
-            table_out[e] = held ? __ldg(a.map + p) : -1;
+            const bool held = j < pages_of(max(seq_lens[s], 0)) && p >= 0 && p < a.num_pages;
+            table_out[e] = held ? a.map[p] : -1;
         }
         return;
     }
-    const long long work = (long long)__ldg(a.moves) * pieces, hop = gridDim.x - remap;
+    const long long work = (long long)*a.moves * pieces, hop = gridDim.x - remap;
     long long w = blockIdx.x - remap;
     int from = 0, to = 0;
     if (w < work) {
-        from = __ldg(a.highs + w / pieces);
-        to = __ldg(a.lows + w / pieces);
+        from = a.highs[w / pieces];
+        to = a.lows[w / pieces];
     }
     while (w < work) {
         const int piece = (int)(w % pieces), src = from, dst = to;
         w += hop;
         if (w < work) {
-            from = __ldg(a.highs + w / pieces);
-            to = __ldg(a.lows + w / pieces);
+            from = a.highs[w / pieces];
+            to = a.lows[w / pieces];
         }
         copy_piece(pb, piece, src, dst);
     }
@@ -498,33 +497,8 @@ PageBufs page_bufs(void *const *bases, const size_t *bytes, int n) {
 
 int pieces_of(const PageBufs &pb) { return pb.units > kPiece ? (pb.units + kPiece - 1) / kPiece : 1; }
 
-cudaLaunchConfig_t cluster_config(int num_pages, cudaLaunchAttribute *attr, cudaStream_t stream) {
-    const unsigned ctas = num_pages <= kOneCtaPages ? 1 : kMaxCtas;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = ctas;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
-// The launch of a call's second kernel.
-const cudaLaunchConfig_t *after_config(unsigned grid, cudaLaunchAttribute *attr, cudaLaunchConfig_t *cfg,
-                                       cudaStream_t stream) {
-    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr->val.programmaticStreamSerializationAllowed = 1;
-    *cfg = {};
-    cfg->gridDim = dim3(grid);
-    cfg->blockDim = dim3(kCopyThreads);
-    cfg->stream = stream;
-    cfg->attrs = attr;
-    cfg->numAttrs = 1;
-    return cfg;
-}
+// CTAs of the cluster that reads the pool's counts.
+unsigned ctas_of(int num_pages) { return num_pages <= kOneCtaPages ? 1 : kMaxCtas; }
 
 }  // namespace
 
@@ -533,9 +507,8 @@ cudaError_t launch_pages_extend(const int32_t *slots, const int32_t *new_lens, i
                                 int32_t *status, cudaStream_t stream) {
     if (n == 0) return cudaSuccess;
     const GrantArgs a{slots, new_lens, n, block_table, n_slots, max_pages, seq_lens, refcount, num_pages, status};
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t cfg = cluster_config(num_pages, &attr, stream);
-    return cudaLaunchKernelEx(&cfg, pages_grant_kernel<false>, a);
+    const unsigned ctas = ctas_of(num_pages);
+    return EarlyLaunch(ctas, kThreads, 0, stream, ctas)(pages_grant_kernel<false>, a);
 }
 
 cudaError_t launch_pages_fork(void *const *bases, const size_t *bytes, int n_bufs, const int32_t *parents,
@@ -544,22 +517,19 @@ cudaError_t launch_pages_fork(void *const *bases, const size_t *bytes, int n_buf
                               cudaStream_t stream) {
     if (n == 0) return cudaSuccess;
     const GrantArgs a{children, parents, n, block_table, n_slots, max_pages, seq_lens, refcount, num_pages, status};
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t cfg = cluster_config(num_pages, &attr, stream);
-    cudaLaunchConfig_t cfg2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, pages_grant_kernel<true>, a);
+    const unsigned ctas = ctas_of(num_pages);
+    const cudaError_t e = EarlyLaunch(ctas, kThreads, 0, stream, ctas)(pages_grant_kernel<true>, a);
     if (e != cudaSuccess) return e;
     const PageBufs pb = page_bufs(bases, bytes, n_bufs);
     const int pieces = pieces_of(pb);
-    return cudaLaunchKernelEx(after_config((unsigned)n * pieces, &attr, &cfg2, stream), pages_fork_kernel, pb, a, pieces);
+    return EarlyLaunch((unsigned)n * pieces, kCopyThreads, 0, stream)(pages_fork_kernel, pb, a, pieces);
 }
 
 cudaError_t launch_pages_free(const int32_t *slots, int n, int32_t *block_table, int n_slots, int max_pages,
                               int32_t *seq_lens, int32_t *refcount, int num_pages, cudaStream_t stream) {
     if (n == 0) return cudaSuccess;
-    pages_free_kernel<<<n, 256, 0, stream>>>(slots, n, block_table, n_slots, max_pages, seq_lens, refcount,
-                                             num_pages);
-    return cudaGetLastError();
+    return EarlyLaunch(n, 256, 0, stream)(pages_free_kernel, slots, n, block_table, n_slots, max_pages, seq_lens,
+                                          refcount, num_pages);
 }
 
 cudaError_t launch_pages_copy(void *const *bases, const size_t *bytes, int n_bufs, const int32_t *src,
@@ -569,8 +539,7 @@ cudaError_t launch_pages_copy(void *const *bases, const size_t *bytes, int n_buf
     const int pieces = pieces_of(pb);
     const long long work = (long long)n * pieces;
     const unsigned grid = (unsigned)(work < (1ll << 30) ? work : (1ll << 30));
-    pages_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(pb, src, dst, n, pieces, num_pages);
-    return cudaGetLastError();
+    return EarlyLaunch(grid, kCopyThreads, 0, stream)(pages_copy_kernel, pb, src, dst, n, pieces, num_pages);
 }
 
 size_t pages_compact_workspace_bytes(int num_pages) { return 16 + 2 * ((size_t)num_pages / 2 + 1) * sizeof(int32_t); }
@@ -581,18 +550,16 @@ cudaError_t launch_pages_compact(void *const *bases, const size_t *bytes, int n_
                                  int32_t *n_used, void *ws, cudaStream_t stream) {
     int32_t *w = static_cast<int32_t *>(ws);
     const CompactArgs a{refs_in, refs_out, map, n_used, num_pages, w, w + 4, w + 4 + num_pages / 2 + 1};
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t cfg = cluster_config(num_pages, &attr, stream);
-    cudaLaunchConfig_t cfg2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, pages_plan_kernel, a);
+    const unsigned ctas = ctas_of(num_pages);
+    const cudaError_t e = EarlyLaunch(ctas, kThreads, 0, stream, ctas)(pages_plan_kernel, a);
     if (e != cudaSuccess) return e;
     const PageBufs pb = page_bufs(bases, bytes, n_bufs);
     const int pieces = pieces_of(pb);
     // one table entry per thread up to a wave's worth of CTAs
     const long long tiles = ((long long)n_slots * max_pages + kCopyThreads - 1) / kCopyThreads;
     const int remap = (int)(tiles < 148 * 4 ? tiles : 148 * 4);
-    return cudaLaunchKernelEx(after_config(remap + 148 * kMoveCtas, &attr, &cfg2, stream), pages_move_kernel, pb, a,
-                              pieces, table_in, table_out, seq_lens, n_slots, max_pages, remap);
+    return EarlyLaunch(remap + 148 * kMoveCtas, kCopyThreads, 0, stream)(
+        pages_move_kernel, pb, a, pieces, table_in, table_out, seq_lens, n_slots, max_pages, remap);
 }
 
 }  // namespace dsa

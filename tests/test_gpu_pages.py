@@ -338,3 +338,96 @@ def test_a_serving_run_of_them_together():
     assert torch.equal(outs[0], outs[1]) and torch.equal(sets[0], sets[1])
     c.free(i32([0, 3, 4, 5]))
     assert not c.refcount.any() and bool((c.block_table == -1).all())
+
+
+@pytest.mark.parametrize("how", ["one stream", "two streams", "a graph", "a graph of two streams"])
+def test_calls_that_follow_each_other_see_what_came_before(how):
+    """Calls begin while the ones before them end: rounds of every call, each
+    on what the last one wrote, give the bits that they give one at a time;
+    between them lie copies, fills and kernels that are not the library's."""
+    S, Hq, Hkv, D, k, rounds = 24, 16, 2, 128, 96, 12
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(11)
+    kv = torch.randn(rounds, 2, S * 40, Hkv, D, generator=gen, device=DEV).to(torch.bfloat16)
+    qs = torch.randn(rounds, S, Hq, D, generator=gen, device=DEV).to(torch.bfloat16)
+    order = torch.stack([torch.randperm(S, generator=gen, device=DEV) for _ in range(rounds)]).to(torch.int32)
+    cu = i32(np.arange(S + 1) * 40)
+    plus = i32([40] * S)
+    picks = torch.arange(k, dtype=torch.int32, device=DEV)
+
+    def run(between, outs, sync, c):
+        for t in (c.k, c.v, c.seq_lens, c.refcount):
+            t.zero_()
+        c.exp.fill_(87)
+        c.block_table.fill_(-1)
+        for r in range(rounds):
+            all_slots = order[r]
+            half = all_slots[:S // 2]
+            calls = [lambda: c.extend(all_slots, c.seq_lens[all_slots.long()] + plus),
+                     lambda: c.append(kv[r, 0], kv[r, 1], cu, slots=all_slots),
+                     lambda: dsa.sparse_gqa_decode_attention_kv8(
+                         qs[r], c.k, c.v, c.exp, c.block_table, c.seq_lens,
+                         (c.seq_lens[:, None] - k + picks).clamp(min=0).to(torch.int32), k, 0.05, outs[r]),
+                     lambda: dsa.sparse_gqa_decode_attention_kv8(
+                         outs[r], c.k, c.v, c.exp, c.block_table, c.seq_lens, picks.repeat(S, 1), k, 0.05, outs[r + 1]),
+                     lambda: c.free(half),
+                     lambda: c.fork(all_slots[S // 2:], half),
+                     lambda: c.free(all_slots[:3]),
+                     lambda: c.compact()]
+            for i, call in enumerate(calls):
+                between(i + r)
+                call()
+                if sync:
+                    torch.cuda.synchronize()
+        if torch.cuda.current_stream() == side:
+            between(3)
+
+    def cache():
+        return dsa.KV8Cache(S * 8 + 20, S, 12, Hkv, D)
+
+    def outputs():
+        return torch.zeros(rounds + 1, S, Hq, D, dtype=torch.bfloat16, device=DEV)
+
+    small, other = torch.ones(64, device=DEV), torch.zeros(64, device=DEV)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    want_c, want = cache(), outputs()
+    run(lambda i: None, want, True, want_c)
+    c, outs = cache(), outputs()
+
+    def between(i):
+        # a copy, a fill, a kernel, nothing; with two streams the next call is
+        # on the other one, behind an event
+        if i % 4 == 0:
+            other.copy_(small)
+        elif i % 4 == 1:
+            other.zero_()
+        elif i % 4 == 2:
+            other.add_(small)
+        if "two streams" in how:
+            here = torch.cuda.current_stream()
+            there = side if here == main else main
+            there.wait_stream(here)
+            torch.cuda.set_stream(there)
+
+    torch.cuda.synchronize()
+    before = torch.cuda.current_stream()
+    if "graph" in how:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            run(between, outs, False, c)
+        for _ in range(3):
+            outs.zero_()
+            g.replay()
+    else:
+        torch.cuda.set_stream(main)
+        try:
+            for _ in range(3):
+                run(between, outs, False, c)
+        finally:
+            torch.cuda.set_stream(before)
+    torch.cuda.synchronize()
+    assert torch.equal(outs.view(torch.int16), want.view(torch.int16)) and bool(want.any())
+    for a, b in ((c.k, want_c.k), (c.v, want_c.v), (c.exp, want_c.exp), (c.block_table, want_c.block_table),
+                 (c.seq_lens, want_c.seq_lens), (c.refcount, want_c.refcount)):
+        assert torch.equal(a, b)
+    assert int(c.seq_lens.max()) > 40
