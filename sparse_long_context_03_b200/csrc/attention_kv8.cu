@@ -34,16 +34,20 @@
 // passes every byte through it twice, and a gather alone then stops at 13 TB/s
 // from L2 against 19 TB/s into registers.
 //
-// What bounds it: instructions.  A warp's 32 keys take about 430 of them, half
-// for the conversions, with three warps to a scheduler (the next step's K and
-// V, in flight, take 64 of 168 registers).  2048 query rows of a 32K sequence
-// with k = 2048, 32 heads on 4 groups of 128 dims: 391 us, 11.0 TB/s of
-// gathered rows (the bf16 kernel's 2 times as many bytes take 555 us for as
-// many rows); 32 sequences decoding: 21.5 us, 3.2 TB/s from HBM (bf16 with its
-// combine: 33 us).  Tried and slower: half the registers and 16 warps (457
-// us); the rows of later steps asked into L2 beforehand (decode 26.7 us);
-// the next step's products with K among this step's with V (464 us: what is
-// loaded then has less time to come).
+// What bounds it: with three warps to a scheduler (the next step's K and V, in
+// flight, take 64 of 168 registers) the loads and the instructions, 400 for a
+// warp's 32 keys and a third of them conversions, overlap only in part: 2048
+// query rows of a 32K sequence with k = 2048, 32 heads on 4 groups of 128 dims
+// take 391 us, 11.0 TB/s of gathered rows; without the arithmetic 282, and 211
+// if a scheduler issued on every cycle.  (The bf16 kernel's 2 times as many
+// bytes take 555 us for as many rows.)  32 sequences decoding: 20.3 us, 3.3
+// TB/s from HBM (bf16 with its combine: 33 us); the same rows' loads alone 15.
+// Tried and slower: half the registers and 16 warps (457 us); V by cp.async
+// through shared memory, read back transposed (446 us, with 16 warps 430); the
+// next step's products with K among this step's with V (464 us: what is loaded
+// then has less time to come); loads under a predicate in place of those that
+// nobody needs (453 us); the rows of later steps asked into L2 beforehand
+// (decode 26.7 us).
 //
 #include <cooperative_groups.h>
 
@@ -190,15 +194,15 @@ template <int D, typename Scales, typename NextK, typename NextV>
 __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Scales scales, NextK next_k,
                                             NextV next_v) {
     // two chains of products for each tile: half the latency
-    float s[2][4] = {}, odd[2][4] = {};
+    float s[2][4], odd[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int w = 0; w < D / 16; ++w) {
             const uint32_t x0 = t[i].k[0][w], x1 = t[i].k[1][w];
             mma_f16_16816(w & 1 ? odd[i] : s[i], e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)x1),
-                          e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)), st.q[w][0],
-                          st.q[w][1]);
+                                e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)(x1 >> 16)),
+                                st.q[w][0], st.q[w][1], w < 2);
         }
         next_k(i);
     }
@@ -322,7 +326,7 @@ struct Join {
     static size_t bytes(int warps, int ctas, int G) {
         const size_t slice = ((size_t)G * (D / 2) + ctas - 1) / ctas;
         if (warps * ctas == 1) return 0;
-        size_t n = (size_t)warps * (kWarp * sizeof(float) + 8 * (sizeof(float2) + sizeof(float)));
+        size_t n = (size_t)warps * (kWarp * sizeof(float) + 8 * sizeof(float2));
         if (ctas > 1) n += ctas * (8 + slice) * sizeof(float2);
         return n;
     }
@@ -362,14 +366,17 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     // of an index read, the selected position; -1 if it is none
     auto position = [&](int s, int step) { return step * 32 + lane < n_vis && s <= t ? s : -1; };
     auto page_of = [&](int s) { return s >= 0 ? bt[s / kPage] : -1; };
+    // a key's scale bytes are looked at a step after they are asked for (at
+    // once: 21.6 us against 20.3 for 32 sequences decoding)
+    constexpr uint32_t kNoKey = 0x10000u;
     int row, some = -1;
-    KeyScales key;
+    uint32_t raw;
     auto resolve = [&](int s, int page) {
         row = -1;
-        key = no_key();
+        raw = kNoKey;
         if (page >= 0 && page < a.num_pages) {
             row = page * kPage + s % kPage;
-            key = key_scales(a.exps[(size_t)(row >> a.block_shift) * a.Hkv + g]);
+            raw = a.exps[(size_t)(row >> a.block_shift) * a.Hkv + g];
         }
         // an entry that selects nothing reads a row that another entry
         // selected, this step's or an earlier one's: with a weight of 0 its
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
         int p0 = page_of(s0), s1 = index_at(step + 2 * nw);
         load_q<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
         for (; step < steps; step += nw) {
-            const KeyScales now = key;
+            const KeyScales now = raw == kNoKey ? no_key() : key_scales(raw);
             // the next step's rows; behind the last step those of the last (a
             // branch around the loads would make them wait: 436 us became 752
             // on a 2048-row prompt chunk)
@@ -427,8 +434,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
     }
     // join the warps' sums: within the CTA, then across the cluster
     float2 *ml = reinterpret_cast<float2 *>(smem + W * S::kWarp);   // [W][8] (ref, l)
-    float *factor = reinterpret_cast<float *>(ml + W * 8);          // [W][8]
-    float2 *recv_ml = reinterpret_cast<float2 *>(factor + W * 8);   // [C][8], from the cluster's CTAs
+    float2 *recv_ml = ml + W * 8;                                   // [C][8], from the cluster's CTAs
     float2 *recv = recv_ml + C * 8;                                 // [C][slice]
     float *own = smem + warp * S::kWarp;
 #pragma unroll
@@ -439,44 +445,30 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
                 make_float2(st.o[w][i], st.o[w][2 + i]);
         if (gid == 0) ml[warp * 8 + 2 * tig + i] = make_float2(st.ref[i], st.l[i]);
     }
-    __syncthreads();
-    float M = kRefNone, L = 0.f;                                    // of head threadIdx.x, if below G
-    if ((int)threadIdx.x < G) {
-        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * 8 + threadIdx.x].x);
-        for (int w = 0; w < W; ++w) {
-            const float2 x = ml[w * 8 + threadIdx.x];
-            const float f = fast_exp2(x.x - M);
-            factor[w * 8 + threadIdx.x] = f;
-            L = fmaf(x.y, f, L);
-        }
-        if (C == 1) {
-            if (lg != nullptr) lg[threadIdx.x] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
-            ml[threadIdx.x] = make_float2(L > 0.f ? 1.f / L : 0.f, 0.f);
-        }
-    }
+    if (C > 1) cluster_wait();
     __syncthreads();
     const int n = G * (D / 2), slice = (n + C - 1) / C;
-    if (C > 1) {
-        cluster_wait();
-        if ((int)threadIdx.x < G)
-            for (int c = 0; c < C; ++c)
-                cluster.map_shared_rank(recv_ml, c)[crank * 8 + threadIdx.x] = make_float2(M, L);
-    }
     for (int e = threadIdx.x; e < n; e += blockDim.x) {
         const int h = e / (D / 2), d = e % (D / 2) * 2;
-        float x = 0.f, y = 0.f;
+        float M = kRefNone, L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * 8 + h].x);
 #pragma unroll 4
         for (int w = 0; w < W; ++w) {
-            const float f = factor[w * 8 + h];
-            const float2 v = *reinterpret_cast<const float2 *>(smem + w * S::kWarp + S::at(h, d));
+            const float2 m = ml[w * 8 + h], v = *reinterpret_cast<const float2 *>(smem + w * S::kWarp + S::at(h, d));
+            const float f = fast_exp2(m.x - M);
+            L = fmaf(m.y, f, L);
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
         }
         if (C == 1) {
-            const float inv = ml[h].x;
+            const float inv = L > 0.f ? 1.f / L : 0.f;
             *reinterpret_cast<uint32_t *>(og + (size_t)h * D + d) = pack_bf16x2(x * inv, y * inv);
+            if (lg != nullptr && d == 0) lg[h] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
         } else {
             cluster.map_shared_rank(recv, e / slice)[crank * slice + e % slice] = make_float2(x, y);
+            // the head's maximum and sum, to the CTA c by the c-th of the head's threads
+            if (d / 2 < C) cluster.map_shared_rank(recv_ml, d / 2)[crank * 8 + h] = make_float2(M, L);
         }
     }
     if (C == 1) return;
@@ -503,23 +495,24 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
 // Where every pair has one warp: a CTA has the pairs of a query's neighbouring
 // groups, one warp each, and looks the query's entries up once for all of
 // them, a block of entries at a time, into shared memory: the rows, and the
-// scales of each group.  Against a warp that looks up for itself this saves 45
+// scales of each group.  Against a warp that looks up for itself this saved 45
 // of 470 instructions per 32 keys, and pays with a block's start, where nothing
 // is under way: 2048 rows (see the head of the file) take 391 us against 420,
 // but 32 rows that are split 24.3 against 22.1, so those keep to
-// sparse_kv8_kernel.  Blocks of 512 entries: 402 us, 1536: 399, 2048: 413.
+// sparse_kv8_kernel.  Blocks of 512 entries: 402 us, 1536: 399, 2048: 413; four
+// entries to a thread looked up at once: 405.
 constexpr int kBlockKeys = 1024;
 constexpr int kMaxGroups = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(const __grid_constant__ Kv8Args a, int block) {
-    extern __shared__ __align__(16) int rows[];     // [block], then the scales, [groups][block]
+    extern __shared__ __align__(16) int rows[];     // [block + 32], then the scales, [groups][block]
     __shared__ int some_row[kMaxGroups];
     wait_for_last();
     const int lane = lane_id(), warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
     const int groups = blockDim.x >> 5, per_row = a.Hkv / groups;
     const int r = blockIdx.x / per_row, g0 = blockIdx.x % per_row * groups, g = g0 + warp, G = a.Hq / a.Hkv;
-    KeyScales *scales = reinterpret_cast<KeyScales *>(rows + block);
+    KeyScales *scales = reinterpret_cast<KeyScales *>(rows + block + 32);
     int b, t;
     if (!query_place(a, r, b, t)) return;
     const int n_vis = max(min(a.k, t + 1), 0);
@@ -551,12 +544,11 @@ __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(con
         for (int w = 0; w < groups; ++w) some = max(some, some_row[w]);
         if (some < 0) continue;                     // nothing is selected here
 
-        // an entry that selects nothing, and the steps behind the last, read a
-        // row that is selected, as in sparse_kv8_kernel
-        auto row_at = [&](int i) {
-            const int x = i < n ? rows[i] : -1;
-            return x < 0 ? some : x;
-        };
+        // an entry that selects nothing, and the step behind the last, read a row
+        // that is selected, as in sparse_kv8_kernel
+        for (int i = threadIdx.x; i < n + 32; i += blockDim.x)
+            if (i >= n || rows[i] < 0) rows[i] = some;
+        __syncthreads();
         auto load = [&](uint32_t(&to)[2][D / 16], const int(&from)[2], const uint8_t *base) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) ldg_stream(to[h], base + (uint64_t)(uint32_t)from[h] * stride);
@@ -566,7 +558,7 @@ __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(con
         int next[2][2];                             // the rows of a step, read before they are needed
         auto look = [&](int at) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) next[i / 2][i % 2] = row_at(at + 8 * i + gid);
+            for (int i = 0; i < 4; ++i) next[i / 2][i % 2] = rows[at + 8 * i + gid];
         };
         look(0);
 #pragma unroll
@@ -614,12 +606,12 @@ cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
     while (a.Hkv % groups != 0) --groups;
     if (sp.warps * sp.ctas == 1 && groups > 1) {
         const int block = a.k < kBlockKeys ? (a.k + 31) / 32 * 32 : kBlockKeys;
-        const size_t smem = block * (sizeof(int) + groups * sizeof(KeyScales));
-        static_assert(kBlockKeys * (sizeof(int) + kMaxGroups * sizeof(KeyScales)) <= 48 << 10, "as below");
+        const size_t smem = (block + 32) * sizeof(int) + block * groups * sizeof(KeyScales);
+        static_assert((kBlockKeys + 32) * sizeof(int) + kBlockKeys * kMaxGroups * sizeof(KeyScales) <= 48 << 10, "as below");
         return EarlyLaunch((unsigned)(pairs / groups), groups * 32, smem, stream)(sparse_kv8_rows_kernel<D>, a, block);
     }
     const size_t smem = Join<D>::bytes(sp.warps, sp.ctas, a.Hq / a.Hkv);
-    static_assert(kMaxWarps * (Join<D>::kWarp + 24) * sizeof(float) + 8 * (D / 2 + 8 + kMaxCluster) * sizeof(float2) <= 48 << 10,
+    static_assert(kMaxWarps * (Join<D>::kWarp + 16) * sizeof(float) + 8 * (D / 2 + 8 + kMaxCluster) * sizeof(float2) <= 48 << 10,
                   "within the default limit of dynamic shared memory");
     // a cluster only where it is needed: an SM holds 8 CTAs of a cluster launch,
     // even of clusters of one, but 12 one-warp CTAs of a plain one

@@ -53,18 +53,26 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
     return make_float2(lo, hi);
 }
 
-// D[16x8] += A[16x16] * B[16x8], fp16 inputs, fp32 accumulators.
+// D[16x8] += A[16x16] * B[16x8], fp16 inputs, fp32 accumulators; with `first`
+// (known when compiling) D = A * B.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                              uint32_t b0, uint32_t b1, bool first = false) {
+    if (first)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // A kernel may be launched to begin while its stream's last one ends (EarlyLaunch
-// below), which hides most of a launch: 21.5 us instead of 24.5 for decoding
+// below), which hides most of a launch: 21.5 us against 24.5 for decoding
 // 32 sequences one call after another.  Each of its threads then waits, before
 // it touches memory, until the last kernel has ended and its writes are seen;
 // and since that kernel may be the one that wrote what this one reads, nothing
