@@ -40,7 +40,7 @@
 // query rows of a 32K sequence with k = 2048, 32 heads on 4 groups of 128 dims
 // take 391 us, 11.0 TB/s of gathered rows; without the arithmetic 282, and 211
 // if a scheduler issued on every cycle.  (The bf16 kernel's 2 times as many
-// bytes take 555 us for as many rows.)  32 sequences decoding: 20.3 us, 3.3
+// bytes take 555 us for as many rows.)  32 sequences decoding: 19.4 us, 3.5
 // TB/s from HBM (bf16 with its combine: 33 us); the same rows' loads alone 15.
 // Tried and slower: half the registers and 16 warps (457 us); V by cp.async
 // through shared memory, read back transposed (446 us, with 16 warps 430); the
@@ -577,31 +577,42 @@ __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(con
     write_pair<D>(st, G, a.out + head * D, a.lse != nullptr ? a.lse + head : nullptr, lane);
 }
 
-// How many warps share a pair, and in how many CTAs: enough that the pairs'
-// warps fill the device once, at most one per 32 keys, in as few CTAs as hold
-// them.  Measured at 32 rows of 4 groups, k = 2048 (12 warps to a pair): 2 CTAs
-// of 6 warps 22.7 us, 4 of 3 23.3, 6 of 2 24.2, 8 of 1 26.8; more warps than
-// the device holds: 2 CTAs of 8 29.9.  One row: 8 CTAs of 8 warps 7.6 us, 4 of
-// 8 8.7, 2 of 8 11.2.  Enough rows take one warp each and join nothing.
+// How many warps share a pair, and in how many CTAs.  Few pairs: as many CTAs
+// as still run all at once, each on an SM that gathers for itself; warps in
+// powers of two, which divide most budgets' steps.  Measured with k = 2048, 4
+// groups of 128 dims, rows read from HBM: 4 rows (16 pairs) 8 CTAs of 4 warps
+// 9.1 us, 8 of 8, of which 16 clusters do not fit, 14.3; 20 rows 4 CTAs of 4
+// 18.6, of 6 23.8; 28 rows one CTA of 8 20.2, 2 of 6 22.4; 64 rows one of 4
+// 39.6, one of 6 39.7, one of 8 40.4; 200 rows one of 4 100, one of 2 115.
+// Many pairs: one warp each, and no join.  Its CTAs of four pairs then take the
+// device by 1776 pairs at a time and about 3.3 times as long as 444 CTAs of one
+// pair and four warps, so that what counts is which of the two ends evenly: 460
+// rows in L2 106 us with four warps and 125 with one, 444 rows 99 and 84.
+// Budgets below 1024 keep to one round of warps when they can: 148 rows with k =
+// 512 in L2, 3 warps 14 us, 4 warps 17.
 struct Split {
     int warps, ctas;
 };
-Split split_of(int64_t pairs, int k, int slots) {
-    const int64_t most = (k + 31) / 32;
-    int64_t want = slots / pairs;
-    want = want < 1 ? 1 : (want > most ? most : want);
-    int ctas = 1;
-    while (ctas < kMaxCluster && want > (int64_t)ctas * kMaxWarps) ctas *= 2;
-    int64_t warps = want / ctas;
-    warps = warps < 1 ? 1 : (warps > kMaxWarps ? kMaxWarps : warps);
-    return {(int)warps, ctas};
+Split split_of(int64_t pairs, int k) {
+    constexpr int kSms = 148, kSmWarps = 12;        // of which a lane's registers allow no more
+    const int steps = (k + 31) / 32;
+    auto rounds = [&](int64_t at_once) { return (pairs + at_once - 1) / at_once; };
+    Split s{4, 1};
+    if (pairs <= 12) s = {8, 8};
+    else if (pairs <= 48) s = {4, 8};
+    else if (pairs <= 96) s = {4, 4};
+    else if (pairs <= kSms) s = {8, 1};
+    else if (pairs > kSms * kSmWarps / 4 && steps < 32) s = {(int)(pairs < kSms * kSmWarps ? kSms * kSmWarps / pairs : 1), 1};
+    else if (33 * rounds(kSms * kSmWarps) <= 10 * rounds(kSms * kSmWarps / 4)) s = {1, 1};
+    while (s.ctas > 1 && s.warps * s.ctas > steps) s.ctas /= 2;
+    if (s.warps > steps) s.warps = steps;
+    return s;
 }
 
 template <int D>
 cudaError_t launch(const Kv8Args &a, cudaStream_t stream) {
-    constexpr int kSlots = 148 * 12;  // SMs x warps that the registers of a lane allow
     const int64_t pairs = (int64_t)a.n_rows * a.Hkv;
-    const Split sp = split_of(pairs, a.k, kSlots);
+    const Split sp = split_of(pairs, a.k);
     int groups = a.Hkv < kMaxGroups ? a.Hkv : kMaxGroups;
     while (a.Hkv % groups != 0) --groups;
     if (sp.warps * sp.ctas == 1 && groups > 1) {

@@ -506,6 +506,26 @@ def test_prefill_of_many_rows(Hq, Hkv, D):
     assert torch.equal(O, O2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("k", [1, 40, 130, 1030])
+@pytest.mark.parametrize("B", [3, 4, 12, 13, 24, 25, 37, 38, 111, 112, 230])
+def test_every_way_to_split_a_pair(B, k):
+    """Batches on both sides of each change of the split, budgets of less than
+    a step to more steps than a pair has warps; some sequences shorter than
+    that, some empty."""
+    rng = np.random.default_rng(B * k)
+    Hq, Hkv, D, block = 12, 4, 64, 32
+    lens = rng.integers(1, 1100, B)
+    lens[rng.integers(0, B)] = 0
+    table, P = deal(lens, rng)
+    kc, vc, exp = random_cache(P, Hkv, D, block, rng, 118, 128)
+    q, qt = bf16(rng.standard_normal((B, Hq, D)))
+    idx = pick_rows(lens, k, rng)
+    idx[0, rng.integers(0, k)] = -1
+    sm = 0.02 / np.sqrt(D)
+    out, lse = decode(qt, [dev(c) for c in (kc, vc, exp)], dev(table), dev(lens, torch.int32), dev(idx), sm)
+    check(out, lse, ref.attention(q, kc, vc, exp, table, idx, np.arange(B), lens - 1, float(np.float32(sm))))
+
+
 def test_prefill_of_many_sequences():
     # more sequences than one round of the search covers, most of them empty
     rng = np.random.default_rng(20)
