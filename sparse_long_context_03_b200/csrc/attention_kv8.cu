@@ -7,11 +7,17 @@
 //     O   = sum_i w_i v_i / sum_i w_i 2^-ev_i,
 //     lse = ln2 * (ref + log2 sum_i w_i 2^-ev_i).
 // Folding ev into the exponent bounds the weights that multiply V by the
-// largest product of weight and scale, so that they fit fp16 whatever the
-// scales; 2^-ev in the sum is exact.  ref moves only when a u exceeds it by
-// more than 15 (weights stay below 2^15 in fp16), and is then put 7 below the
-// largest u: nearly every block keeps it, and the check is one vote instead
-// of a maximum over the warp.
+// largest product of weight and scale; 2^-ev in the sum is exact.  ref moves
+// only when a u exceeds it by more than 15 (weights stay below 2^15 in fp16),
+// and is then put 7 below the largest u: nearly every block keeps it, and the
+// check is one vote instead of a maximum over the warp.  A weight below fp16's
+// normal range is off by at most 2^-25, against 2^7 of the key that set ref:
+// 2^-32 of the softmax where V's scales are alike, 2^-28 where this key's is up
+// to 2^4 below that one's.  Keys of scales farther below may be all that there
+// is in a dim (the scale may be one outlier's, zeros around it), so in steps
+// that have such keys the small weights are multiplied in further windows of
+// 2^24 (take_small_weights): with a fifth of the pages 2^24 above the others
+// 2048 rows take 828 us in place of 392.
 //
 // e4m3 converts to fp16 without loss, and the products run on fp16 matrix
 // instructions with fp32 sums.  (The warp-level 8-bit matrix instructions are
@@ -21,7 +27,7 @@
 // multiplied by the power of two that puts its largest value into [2^14,
 // 2^15), after which fp16 holds every bf16 value that is 2^-30 of the largest
 // or more exactly; the weights are rounded to fp16 (2^-11, an eighth of what
-// bf16 would lose), the sums are of the unrounded weights.
+// bf16 would lose; small ones as above), the sums are of the unrounded weights.
 //
 // Work unit: one warp owns 32 keys of a (query, KV group) pair at a time, all
 // G <= 8 heads at once (keys on the matrix M dimension, heads on N = 8).  The
@@ -51,6 +57,8 @@
 //
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv8.cuh"
 
@@ -63,6 +71,10 @@ namespace {
 constexpr int kMaxWarps = 8;     // warps of a CTA
 constexpr int kMaxCluster = 8;   // CTAs of a cluster
 constexpr float kRefNone = -1e30f;
+constexpr float kF16Normal = 6.103515625e-5f;   // 2^-14: fp16's least normal value
+constexpr float kUp = 16777216.f;               // 2^24: from one window of weights to the next
+constexpr int kNearLog2 = 4;                     // scales of V no more than 2^4 apart: one window is enough
+constexpr float kNear = 1 << kNearLog2;
 
 struct Kv8Args {
     const uint16_t *q;
@@ -125,6 +137,7 @@ struct Kv8State {
     float c[2];                  // c / (the power of two on Q's row), of the two heads
     float o[D / 16][4];
     float ref[2], l[2];
+    float far;                   // 2^4 / (the largest scale of V among the keys that moved ref)
 };
 
 template <int D>
@@ -135,6 +148,7 @@ __device__ __forceinline__ void clear_sums(Kv8State<D> &st) {
         for (int i = 0; i < 4; ++i) st.o[w][i] = 0.f;
     st.ref[0] = st.ref[1] = kRefNone;
     st.l[0] = st.l[1] = 0.f;
+    st.far = INFINITY;
 }
 
 template <int D>
@@ -186,11 +200,73 @@ __device__ __forceinline__ KeyScales key_scales(uint32_t e) {
     return {(e & 0xFFu) << 23 | (254u - (e >> 8)) << 7, (float)(int)(e >> 8) - 127.f};
 }
 
-// Attends to the 32 keys in t[0] and t[1]; scales(i, h) are those of the
+// V's bytes of a tile's two words of eight keys each, as the matrix
+// instruction's operand: the transpose takes them from a lane per key to a lane
+// per two keys, two dims at a time; the byte permute makes pairs of keys of one
+// dim.
+__device__ __forceinline__ void mma_v(float (&d)[4], uint32_t v0, uint32_t v1, uint32_t b0, uint32_t b1,
+                                      bool first = false) {
+    const uint32_t x = __byte_perm(movmatrix_trans(v0), 0u, 0x3120), y = __byte_perm(movmatrix_trans(v1), 0u, 0x3120);
+    mma_f16_16816(d, e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                  e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b0, b1, first);
+}
+
+// Keys whose weights are below fp16's normal range: their weights are added to
+// the sums, multiplied with V in windows of 2^24, each moved into that range,
+// and their u is set to -inf, so that what follows passes them by.  After four
+// windows the rest is below 2^-110 on a scale on which the reference's key has
+// 2^7, and so below 2^-37 of the softmax whatever the scales.
+template <int D>
+__device__ __forceinline__ void take_small_weights(Kv8State<D> &st, const Tile<D> (&t)[2], float (&u)[2][4],
+                                                   const float (&iv)[2][2]) {
+    float up = kUp;
+#pragma unroll 1
+    for (int n = 0; n < 4; ++n, up *= kUp) {
+        uint32_t b[2][2];
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float p = fast_exp2(u[i][2 * h + j] - st.ref[j]);
+                    x[j] = p < kF16Normal ? p * up : 0.f;
+                    some = some || (x[j] > 0.f && x[j] < kF16Normal * kUp);
+                    if (!(x[j] >= kF16Normal && x[j] < kF16Normal * kUp)) x[j] = 0.f;
+                }
+                b[i][h] = movmatrix_trans(pack_f16x2(x[0], x[1]));
+            }
+        if (!__any_sync(0xFFFFFFFFu, some)) break;  // none in this window or below it
+        const float down = 1.f / up;
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+            float sum[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mma_v(sum, t[i].v[0][w], t[i].v[1][w], b[i][0], b[i][1], i == 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st.o[w][j] = fmaf(sum[j], down, st.o[w][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p = fast_exp2(u[i][j] - st.ref[j & 1]);
+            if (p < kF16Normal) {                   // not so for a NaN
+                st.l[j & 1] = fmaf(p, iv[i][j >> 1], st.l[j & 1]);
+                u[i][j] = -INFINITY;
+            }
+        }
+}
+
+// Attends to the 32 keys in t[0] and t[1]; kFar: V's scales may lie more than
+// 2^4 below those seen before; scales(i, h) are those of the
 // lane's key gid + 8 h of t[i], next_k(i) and next_v(i) issue the loads that
 // take t[i]'s place, as soon as its registers are read (after both tiles: 22.1
 // us against 21.5 for 32 sequences decoding).
-template <int D, typename Scales, typename NextK, typename NextV>
+template <int D, bool kFar, typename Scales, typename NextK, typename NextV>
 __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Scales scales, NextK next_k,
                                             NextV next_v) {
     // two chains of products for each tile: half the latency
@@ -224,27 +300,42 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Sc
     float mx[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmaxf(u[0][i], u[0][2 + i]), fmaxf(u[1][i], u[1][2 + i]));
-    if (__any_sync(0xFFFFFFFFu, fmaxf(mx[0] - st.ref[0], mx[1] - st.ref[1]) > 15.f)) {
+    // 1 / (V's scale), the largest among the lane's keys (0 for a key that does not exist)
+    const float farthest = fmaxf(fmaxf(iv[0][0], iv[0][1]), fmaxf(iv[1][0], iv[1][1]));
+    const bool move = fmaxf(mx[0] - st.ref[0], mx[1] - st.ref[1]) > 15.f;
+    if (__any_sync(0xFFFFFFFFu, move || (kFar && farthest > st.far))) {
+        if (!kFar || __any_sync(0xFFFFFFFFu, move)) {
+            float nearest = INFINITY;
+            if (kFar) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], o));
-        }
-        float alpha[2];
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float ref = mx[i] - st.ref[i] > 15.f ? mx[i] - 7.f : st.ref[i];
-            alpha[i] = fast_exp2(st.ref[i] - ref);
-            st.ref[i] = ref;
-            st.l[i] *= alpha[i];
-        }
+                    for (int h = 0; h < 2; ++h) nearest = iv[i][h] > 0.f ? fminf(nearest, iv[i][h]) : nearest;
+            }
 #pragma unroll
-        for (int w = 0; w < D / 16; ++w) {
-            st.o[w][0] *= alpha[0];
-            st.o[w][1] *= alpha[1];
-            st.o[w][2] *= alpha[0];
-            st.o[w][3] *= alpha[1];
+            for (int o = 4; o < 32; o <<= 1) {
+                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], o));
+                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], o));
+                if (kFar) nearest = fminf(nearest, __shfl_xor_sync(0xFFFFFFFFu, nearest, o));
+            }
+            if (kFar) st.far = fminf(st.far, kNear * nearest);
+            float alpha[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float ref = mx[i] - st.ref[i] > 15.f ? mx[i] - 7.f : st.ref[i];
+                alpha[i] = fast_exp2(st.ref[i] - ref);
+                st.ref[i] = ref;
+                st.l[i] *= alpha[i];
+            }
+#pragma unroll
+            for (int w = 0; w < D / 16; ++w) {
+                st.o[w][0] *= alpha[0];
+                st.o[w][1] *= alpha[1];
+                st.o[w][2] *= alpha[0];
+                st.o[w][3] *= alpha[1];
+            }
         }
+        if (kFar && __any_sync(0xFFFFFFFFu, farthest > st.far)) take_small_weights<D>(st, t, u, iv);
     }
     uint32_t b[2][2];
 #pragma unroll
@@ -256,17 +347,10 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Sc
             st.l[1] = fmaf(p1, iv[i][h], st.l[1]);
             b[i][h] = movmatrix_trans(pack_f16x2(p0, p1));
         }
-    // the transpose takes V from a lane per key to a lane per two keys, two
-    // dims at a time; the byte permute makes pairs of keys of one dim
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int w = 0; w < D / 16; ++w) {
-            const uint32_t x = __byte_perm(movmatrix_trans(t[i].v[0][w]), 0u, 0x3120);
-            const uint32_t y = __byte_perm(movmatrix_trans(t[i].v[1][w]), 0u, 0x3120);
-            mma_f16_16816(st.o[w], e4m3x2_to_f16x2((uint16_t)x), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
-                          e4m3x2_to_f16x2((uint16_t)y), e4m3x2_to_f16x2((uint16_t)(y >> 16)), b[i][0], b[i][1]);
-        }
+        for (int w = 0; w < D / 16; ++w) mma_v(st.o[w], t[i].v[0][w], t[i].v[1][w], b[i][0], b[i][1]);
         next_v(i);
     }
 }
@@ -413,7 +497,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
             s0 = position(s1, step + 2 * nw);
             p0 = page_of(s0);
             s1 = index_at(step + 3 * nw);
-            attend_keys<D>(
+            attend_keys<D, true>(
                 st, tile,
                 [&](int i, int h) {
                     const int from = 16 * i + 8 * h + (lane >> 2);
@@ -501,11 +585,15 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
 // but 32 rows that are split 24.3 against 22.1, so those keep to
 // sparse_kv8_kernel.  Blocks of 512 entries: 402 us, 1536: 399, 2048: 413; four
 // entries to a thread looked up at once: 405.
+// A block whose scales of V all lie within 2^4 of the largest so far takes the
+// loop without the check for those below (checked at each step: 408 us).  Four
+// CTAs to an SM with 64 dims (without that bound the compiler takes 153
+// registers and three fit: 341 us against 306 for 2048 rows).
 constexpr int kBlockKeys = 1024;
 constexpr int kMaxGroups = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(const __grid_constant__ Kv8Args a, int block) {
+__global__ void __launch_bounds__(kMaxGroups * 32, D == 64 ? 4 : 3) sparse_kv8_rows_kernel(const __grid_constant__ Kv8Args a, int block) {
     extern __shared__ __align__(16) int rows[];     // [block + 32], then the scales, [groups][block]
     __shared__ int some_row[kMaxGroups];
     wait_for_last();
@@ -523,6 +611,7 @@ __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(con
     clear_sums<D>(st);
     load_q<D>(st, a.q + ((size_t)r * a.Hq + (size_t)g * G) * D, G, a.scale_log2, lane);
 
+    int top = -1000;                                // the largest scale of V so far, its exponent
     for (int base = 0; base < n_vis; base += block) {
         const int n = (min(block, n_vis - base) + 31) / 32 * 32;
         if (base > 0) __syncthreads();              // the last block's keys are no longer read
@@ -565,11 +654,29 @@ __global__ void __launch_bounds__(kMaxGroups * 32, 3) sparse_kv8_rows_kernel(con
         for (int i = 0; i < 2; ++i) load(tile[i].k, next[i], kg);
 #pragma unroll
         for (int i = 0; i < 2; ++i) load(tile[i].v, next[i], vg);
-        for (int at = 0; at < n; at += 32) {
-            look(at + 32);
-            attend_keys<D>(
-                st, tile, [&](int i, int h) { return mine[at + 16 * i + 8 * h]; },
-                [&](int i) { load(tile[i].k, next[i], kg); }, [&](int i) { load(tile[i].v, next[i], vg); });
+        // the scales of V in this block, while the first rows are on their way
+        float hi = -1000.f, lo = 1000.f;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) {
+            const float ev = scales[warp * block + i].ev;
+            hi = fmaxf(hi, ev);
+            lo = fminf(lo, ev > -INFINITY ? ev : lo);
+        }
+        top = max(top, __reduce_max_sync(0xFFFFFFFFu, (int)hi));
+        const bool near = __all_sync(0xFFFFFFFFu, top - (int)lo <= kNearLog2);
+        auto attend = [&](auto far) {
+            for (int at = 0; at < n; at += 32) {
+                look(at + 32);
+                attend_keys<D, far>(
+                    st, tile, [&](int i, int h) { return mine[at + 16 * i + 8 * h]; },
+                    [&](int i) { load(tile[i].k, next[i], kg); }, [&](int i) { load(tile[i].v, next[i], vg); });
+            }
+        };
+        if (near) {
+            attend(std::false_type{});
+        } else {
+            st.far = exp2f((float)(kNearLog2 - top));
+            attend(std::true_type{});
         }
     }
     sum_weights<D>(st);
