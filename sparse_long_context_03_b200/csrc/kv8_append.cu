@@ -88,12 +88,14 @@ __global__ void __launch_bounds__(T) kv8_append_kernel(const __grid_constant__ A
         t0 = a.cu[b];
         n_new = a.cu[b + 1] - t0;
         j = u - ((t0 >> a.shift) + 2 * b);
-        if (t0 < 0 || n_new <= 0 || n_new > a.n_tokens - t0) return;
+        if (t0 < 0 || n_new <= 0 || n_new > a.n_tokens - t0 || (unsigned)j > (unsigned)(n_new >> a.shift) + 1) return;
     }
-    const int pos0 = a.seq_lens[b] - n_new; // the first new token's position
-    if (pos0 < 0 || pos0 >= a.max_pages * kPage) return;
-    const int start = ((pos0 >> a.shift) + j) << a.shift;           // the block's first position
-    const int lo = max(start, pos0), hi = min(start + (1 << a.shift), pos0 + n_new);
+    const int len = a.seq_lens[b];
+    if (len <= 0) return;
+    const int pos0 = len - n_new;           // the first new token's position; tokens at negative ones have no place
+    if (pos0 >= a.max_pages * kPage) return;
+    const int start = ((pos0 >> a.shift) + j) * (1 << a.shift);     // the block's first position
+    const int lo = max(start, max(pos0, 0)), hi = min(start + (1 << a.shift), len);
     if (lo >= hi || start >= a.max_pages * kPage) return;
     const int m = hi - lo, m_old = lo - start, tok = t0 + (lo - pos0);  // tok: the first among the new tokens
     const bool keys = g == a.Hkv;
