@@ -41,6 +41,10 @@ constexpr int kOneCtaPages = 4096;
 constexpr int kHash = 2 * kPagesMaxEntries;
 static_assert(kPagesMaxEntries <= kThreads, "one entry per thread");
 
+// Sums of wanted pages stop here, above every pool's size: 1024 entries may
+// together want more than 31 bits hold.
+constexpr int kMostWanted = 1 << 25;
+
 enum : int32_t { kOk = 0, kNoSpace = 1, kBad = 2 };
 
 __device__ __forceinline__ int pages_of(int tokens) { return tokens / kPageTokens + (tokens % kPageTokens != 0); }
@@ -188,11 +192,11 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
         first_of[i] = FORK ? to / kPageTokens : pages_of(len);
     }
     slot_of[i] = s;
-    int v = need;
+    int v = min(need, kMostWanted);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += x;
+        if (lane >= o) v = min(v + x, kMostWanted);
     }
     if (lane == 31) warp_sum[warp] = v;
     __syncthreads();
@@ -200,10 +204,10 @@ __global__ void __launch_bounds__(kThreads) pages_grant_kernel(const __grid_cons
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xFFFFFFFFu, w, o);
-        if (lane >= o) w += x;
+        if (lane >= o) w = min(w + x, kMostWanted);
     }
     const int wanted = __shfl_sync(0xFFFFFFFFu, w, 31);
-    v += warp == 0 ? 0 : __shfl_sync(0xFFFFFFFFu, w, warp - 1);
+    v = min(v + (warp == 0 ? 0 : __shfl_sync(0xFFFFFFFFu, w, warp - 1)), kMostWanted);
     upto[i] = v;
 
     // count the free pages, unless nobody wants one
