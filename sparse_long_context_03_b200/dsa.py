@@ -859,10 +859,14 @@ class KV8Cache:
         return page_map, n_used
 
     def append(self, K, V, cu_seqlens=None, k8=None, k_scale=None, slots=None):
-        """kv8_append of the last tokens of the sequences (extend comes first)."""
+        """kv8_append of the last tokens of the sequences (extend comes first).
+        k8 and k_scale are given exactly when the cache holds indexer keys: a
+        page's earlier keys are another sequence's.  A slot is named once."""
+        if (self.k8 is None) != (k8 is None):
+            raise ValueError("k8: the cache holds " + ("no indexer keys (dI)" if self.k8 is None else
+                                                       "indexer keys (dI), and these tokens come without"))
         table, lens = self._rows(slots)
-        kv8_append(K, V, self.k, self.v, self.exp, table, lens, cu_seqlens, k8, k_scale,
-                   self.k8 if k8 is not None else None, self.k_scale if k8 is not None else None)
+        kv8_append(K, V, self.k, self.v, self.exp, table, lens, cu_seqlens, k8, k_scale, self.k8, self.k_scale)
 
     def prefill(self, Q, idx, cu_seqlens, O, sm_scale=None, lse=None, slots=None):
         """sparse_gqa_prefill_kv8 of all packed query rows."""
