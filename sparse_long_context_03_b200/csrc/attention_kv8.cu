@@ -70,7 +70,7 @@ namespace {
 
 constexpr int kMaxWarps = 8;     // warps of a CTA
 constexpr int kMaxCluster = 8;   // CTAs of a cluster
-constexpr float kRefNone = -1e30f;
+constexpr float kRefNone = -3.402823466e38f;    // the least float: every finite u is above it
 constexpr float kF16Normal = 6.103515625e-5f;   // 2^-14: fp16's least normal value
 constexpr float kUp = 16777216.f;               // 2^24: from one window of weights to the next
 constexpr int kNearLog2 = 4;                     // scales of V no more than 2^4 apart: one window is enough
