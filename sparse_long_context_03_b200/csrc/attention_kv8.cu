@@ -294,8 +294,9 @@ __device__ __forceinline__ void attend_keys(Kv8State<D> &st, Tile<D> (&t)[2], Sc
             const KeyScales x = scales(i, h);
             const float ks = __uint_as_float(x.scales & 0xFFFF0000u);
             iv[i][h] = __uint_as_float(x.scales << 16);
-            u[i][2 * h] = fmaf(s[i][2 * h], st.c[0] * ks, x.ev);
-            u[i][2 * h + 1] = fmaf(s[i][2 * h + 1], st.c[1] * ks, x.ev);
+            // K's scale first: the product is exact, and c with it could pass what a float holds
+            u[i][2 * h] = fmaf(s[i][2 * h] * ks, st.c[0], x.ev);
+            u[i][2 * h + 1] = fmaf(s[i][2 * h + 1] * ks, st.c[1], x.ev);
         }
     float mx[2];
 #pragma unroll
