@@ -122,10 +122,8 @@ __device__ __forceinline__ void load_half(uint32_t (&to)[2][D / 16], int row, in
 }
 
 // Running state of one warp: lane (gid, tig) holds heads 2 tig and 2 tig + 1;
-// o[w] are the products of one matrix instruction, for dims d = (gid / 2) *
-// D/4 + 4 w + gid % 2 (o[w][0], o[w][1]) and d + 2 (o[w][2], o[w][3]) of the
-// two heads; at the end lanes of even and odd gid exchange one of the two, so
-// that each has dims dim_of(gid, w) and the next.
+// o[w] are the products of one matrix instruction, for dims d = dim_of(gid, w)
+// (o[w][0], o[w][1]: the two heads) and d + 1 (o[w][2], o[w][3]).
 template <int D>
 __device__ __forceinline__ int dim_of(int gid, int w) {
     return (gid >> 1) * (D / 4) + 4 * w + 2 * (gid & 1);
@@ -702,7 +700,9 @@ struct Split {
     int warps, ctas;
 };
 Split split_of(int64_t pairs, int k) {
-    constexpr int kSms = 148, kSmWarps = 12;        // of which a lane's registers allow no more
+    // 12 warps to an SM: what 168 registers allow with 128 dims (with 64 dims the
+    // one-warp rows have 16; what is measured above is of 128)
+    constexpr int kSms = 148, kSmWarps = 12;
     const int steps = (k + 31) / 32;
     auto rounds = [&](int64_t at_once) { return (pairs + at_once - 1) / at_once; };
     Split s{4, 1};

@@ -270,7 +270,7 @@ struct PageBufs {
     unsigned long long page_bytes[kPagesMaxBufs];
     int shift[kPagesMaxBufs];
     int units_end[kPagesMaxBufs];   // units of buffers 0..i
-    int n, units;
+    int units;
 };
 
 constexpr int kCopyThreads = 256;
@@ -486,7 +486,6 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const __grid_c
 
 PageBufs page_bufs(void *const *bases, const size_t *bytes, int n) {
     PageBufs pb{};
-    pb.n = n;
     for (int i = 0; i < n; ++i) {
         int sh = 4;
         while (sh > 0 && ((reinterpret_cast<uintptr_t>(bases[i]) | bytes[i]) & ((1u << sh) - 1))) --sh;
