@@ -411,8 +411,9 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_noalloc(const uint16_t *q,
  *   k_scale_cache the new tokens' indexer keys [n_tokens, dI] and scales
  *                 [n_tokens], copied to their places in [num_pages, 64, dI]
  *                 and [num_pages, 64]; all four or none (then dI is unused)
- * A token at a negative position, past the block table, or on a page outside
- * [0, num_pages) is dropped.  A page that receives tokens must belong to one
+ * A token at a negative position (a sequence may be shorter than its new
+ * tokens), past the block table, or on a page outside [0, num_pages) is
+ * dropped, the others of its sequence are not.  A page that receives tokens must belong to one
  * sequence only (dsa_pages_fork keeps it so).  Slots behind a sequence's last
  * token are left as they were.  Supported: D in {64, 128}, Hkv <= 1024, dI in
  * {32, 64, 128}.
@@ -428,7 +429,11 @@ DSA_API dsa_status_t dsa_kv8_append(const uint16_t *K, int64_t ld_k, const uint1
  * with the same treatment of index entries, pages and empty rows, and without
  * a workspace (a row's splits are joined on chip).  kv_exp is 2-byte aligned,
  * q and out 16-byte, k_cache8 and v_cache8 32-byte.  k <= 2^30.  Cached scale
- * exponents outside 87..167 give unspecified results. */
+ * exponents outside 87..167 give unspecified results.  Within a head's query
+ * row, values below 2^-30 of the largest may lose bits.  Scores and sums are
+ * held in fp32, the weights that multiply V in fp16: beside its bf16 rounding a
+ * dim of the output is off for that by 2^-11 of the weighted mean of |V| in that
+ * dim and by 2^-28 of the largest |V| there for each selected key, at most. */
 DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_kv8(const uint16_t *q, const uint8_t *k_cache8,
                                                  const uint8_t *v_cache8, const uint8_t *kv_exp, int scale_block,
                                                  const int32_t *block_table, int max_pages, int num_pages,
@@ -442,7 +447,10 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_attention_kv8(const uint16_t *q, cons
  * last of its seq_lens[b] cached tokens: row r of it stands at position t =
  * seq_lens[b] - cu_seqlens[b+1] + r and sees the cached tokens 0..t.  idx rows
  * hold positions within the sequence; only the first min(k, t+1) entries are
- * visited and entries outside [0, t] are skipped.
+ * visited and entries outside [0, t] are skipped.  From paged indexer keys they
+ * are selected by dsa_decode_indexer_scores and dsa_topk, or the whole chain
+ * below, with a batch row for each query token: its sequence's block-table row
+ * and t + 1 as the length.
  *   Q, O [n_rows, Hq, D], idx [n_rows, k], lse [n_rows, Hq] (may be NULL):
  *        packed rows row_begin .. row_begin + n_rows - 1
  *   block_table [nseq, max_pages], seq_lens [nseq]
@@ -475,7 +483,8 @@ DSA_API dsa_status_t dsa_sparse_gqa_decode_kv8(const uint16_t *q, const uint8_t 
  *   seq_lens      [n_slots] int32, 0 = empty slot
  * All three start as zeros (block_table: -1) and are changed by the calls
  * below, on the device; a call sees the state that earlier calls on its stream
- * left.  Free pages are granted lowest id first, to the entries of a call in
+ * left.  Lengths only grow, until a slot is freed: one lowered by hand would
+ * leave the pages behind it counted and out of reach.  Free pages are granted lowest id first, to the entries of a call in
  * their order, so every result is determined.  A page that is only partly
  * filled belongs to one sequence: forking copies it, so that appending never
  * writes to a page that another sequence reads.

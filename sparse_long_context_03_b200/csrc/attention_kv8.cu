@@ -44,9 +44,9 @@
 // flight, take 64 of 168 registers) the loads and the instructions, 400 for a
 // warp's 32 keys and a third of them conversions, overlap only in part: 2048
 // query rows of a 32K sequence with k = 2048, 32 heads on 4 groups of 128 dims
-// take 391 us, 11.0 TB/s of gathered rows; without the arithmetic 282, and 211
+// take 392 us, 11.0 TB/s of gathered rows; without the arithmetic 282, and 211
 // if a scheduler issued on every cycle.  (The bf16 kernel's 2 times as many
-// bytes take 555 us for as many rows.)  32 sequences decoding: 19.4 us, 3.5
+// bytes take 555 us for as many rows.)  32 sequences decoding: 19.2 us, 3.5
 // TB/s from HBM (bf16 with its combine: 33 us); the same rows' loads alone 15.
 // Tried and slower: half the registers and 16 warps (457 us); V by cp.async
 // through shared memory, read back transposed (446 us, with 16 warps 430); the
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(384, 1) sparse_kv8_kernel(const __grid_constan
 // them, a block of entries at a time, into shared memory: the rows, and the
 // scales of each group.  Against a warp that looks up for itself this saved 45
 // of 470 instructions per 32 keys, and pays with a block's start, where nothing
-// is under way: 2048 rows (see the head of the file) take 391 us against 420,
+// is under way: 2048 rows (see the head of the file) took 391 us against 420,
 // but 32 rows that are split 24.3 against 22.1, so those keep to
 // sparse_kv8_kernel.  Blocks of 512 entries: 402 us, 1536: 399, 2048: 413; four
 // entries to a thread looked up at once: 405.

@@ -13,7 +13,7 @@
 // values stay in registers between the maximum and the conversion, so K and V
 // are read once.  One more CTA per block copies the indexer's keys.  Bound by
 // HBM for prompts (2 bytes in, 1 byte out per value): a 32K prompt of 4 heads
-// of 128 takes 20.3 us, 5.1 TB/s, against 16 us for a plain copy of as many
+// of 128 takes 20.4 us, 5.1 TB/s, against 16 us for a plain copy of as many
 // bytes.  (K and V in CTAs of their own, with divisions in place of shifts,
 // took 27.6 us: more instructions than the loads could hide.)  Single tokens
 // are bound by the chain of loads length, page, scale: 1.8 us for 32 sequences.

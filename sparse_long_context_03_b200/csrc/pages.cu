@@ -13,12 +13,12 @@
 // over their stretch once more and write the ids.  The entries (at most 1024,
 // one per thread) are worked out by every CTA for itself.  Bound by latency:
 // loads, a barrier across the cluster, loads again.  Freeing 32 sequences and
-// granting their room anew from 13K pages takes 8.5 us; with one CTA and a
+// granting their room anew from 13K pages takes 8.7 us; with one CTA and a
 // load per round of 32 ids it took 20.7.
 //
 // Copying moves pages in pieces of 1024 units, four 16-byte loads in flight to
 // a thread.  2048 pages of 69 KB: 49.4 us, 5.7 TB/s read and written, 88 % of a
-// plain copy's 6.55.  Compacting 720 of 1800 pages: 24.9 us, of which the moved
+// plain copy's 6.55.  Compacting 720 of 1800 pages: 24.7 us, of which the moved
 // bytes' copy would take 15.
 #include <cooperative_groups.h>
 
